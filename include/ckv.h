@@ -399,6 +399,121 @@ ckv_status ckv_attend_rows_static(const ckv_config* cfg, const void* q, const vo
                                   int n, const int32_t* rows_host, const int32_t* n_rows_host,
                                   int max_rows, float* out, void* stream);
 
+/* ---- Rows into the caches, and the cache held in 4 bits ------------------
+ * The decode step starts where "row n-1 of K and V already holds the new
+ * token".  The calls below make those rows (and q) from a projection's
+ * output, hold the caches in 4 bits, and attend over such caches.  The paper
+ * has no counterpart.  They need no context: of a ckv_config they read batch,
+ * n_q_heads, n_kv_heads, head_dim (128), n_max, kv_dtype (element type of q,
+ * of the rows and of 16/32-bit caches) and device, and what else a call
+ * names.  They run on cfg->device whatever device is current (restored on
+ * return), only enqueue work on `stream`, allocate nothing and can be
+ * captured into a graph.  n_max may be at most 2^31 - 65, batch * n_q_heads at
+ * most 2^20; pointers are 16-byte aligned.
+ *
+ * The 4-bit cache of K (or of V) is one buffer of ckv_kv4_bytes(cfg, group)
+ * bytes, group 32, 64 or 128 neighbouring channels sharing a scale: codes
+ * [B][H_kv][R][64 bytes], then (scale, middle) pairs of bfloat16
+ * [B][H_kv][R][128 / group] with R = n_max rounded up to 16.  Of a group of
+ * values x: scale = the smallest bfloat16 >= (max - min) / 15, middle =
+ * min + 8 scale rounded to float and to bfloat16, code = (x - middle) / scale
+ * rounded to nearest even and clamped to [-8, 7], value = middle + scale *
+ * code.  It is off by at most scale / 2 plus the rounding of the middle
+ * (2^-9 |middle|).  A group that holds an infinity or a NaN reads back as
+ * NaN; values beyond 2^126 may read back as infinities.
+ * Byte order of a row (h = 0 is the low nibble, codes in two's complement):
+ * K: channel 32 j + 8 t + 4 h + i is in byte 16 t + 4 j + i; V: channel
+ * 32 j + 4 g + 2 i + h is in byte 8 g + 2 j + i. */
+size_t ckv_kv4_bytes(const ckv_config* cfg, int group);   /* 0 for a bad argument */
+
+/* Queries and keys normalised per head and rotated to their positions, keys
+ * and values written to the caches, in one pass over a projection's output.
+ * For each token (b, t) and each head of q and k:
+ *   y  = x / sqrt(mean(x^2) + eps) * weight         (weight null: y = x)
+ *   a' = rot_scale (a cos f - b sin f), b' = rot_scale (b cos f + a sin f)
+ * for the rot_dim / 2 pairs (a, b) of channels (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) when interleaved, f = pos[b][t] * inv_freq[i]; channels from
+ * rot_dim on stay y.  32-bit arithmetic with one rounding at the end; the
+ * angle is formed and reduced in 64 bits.  v is taken as it is.
+ * q goes to q_out, k and v to row pos[b][t] of the caches K and V
+ * ([B][H_kv][n_max][D]), of the 4-bit caches K4 and V4, or of both (the
+ * 4-bit rows then hold the rows of K and V, quantised; without K and V what
+ * those would hold).  A token whose pos is outside [0, n_max) is padding:
+ * nothing of it is read or written, its q_out row stays as it was.  Two tokens of one
+ * sequence at the same position leave an unspecified mixture in that row.
+ * Strides are in elements, for batch, token and head; channels are
+ * contiguous; a multiple of 16 bytes each.  q_out may be q (in place).
+ * Errors: CKV_ERR_INVALID_ARG (also: K without V, K4 without V4, no cache at
+ * all, an inv_freq that is not finite), CKV_ERR_CUDA. */
+typedef struct {
+    int n_tokens;                    /* T >= 0 tokens of each sequence                      */
+    int rot_dim;                     /* rotated channels: 0, 16, .., 128                    */
+    int interleaved;                 /* pairs (2i, 2i+1) instead of (i, i + rot_dim/2)      */
+    int group;                       /* of the 4-bit caches                                 */
+    float eps, rot_scale;
+    const double* inv_freq_host;     /* [rot_dim / 2], radians per position (host)          */
+    const void *q, *k, *v;           /* [B][T][heads][D] by strides                         */
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    const int32_t* pos;              /* [B][T]                                              */
+    const void *q_weight, *k_weight; /* [D] kv_dtype, or null: no norm                      */
+    void* q_out;                     /* [B][T][H_q][D] by strides                           */
+    int64_t q_out_stride[3];
+    void *K, *V;                     /* 16/32-bit caches, or both null                      */
+    void *K4, *V4;                   /* 4-bit caches, or both null                          */
+} ckv_qkv;
+ckv_status ckv_qk_norm_rope(const ckv_config* cfg, const ckv_qkv* x, void* stream);
+
+/* Rows into the 4-bit caches: k and v of n_tokens tokens of each sequence
+ * ([B][T][H_kv][D] by strides in elements for batch, token and head, host
+ * arrays of 3; a cache [B][H_kv][n_max][D] is such a source too) quantised
+ * to row pos[b][t] (device [B][T]; null: rows 0 .. n_tokens-1).  Padding and
+ * repeated positions as in ckv_qk_norm_rope.
+ * Errors: CKV_ERR_INVALID_ARG, CKV_ERR_CUDA. */
+ckv_status ckv_kv4_write(const ckv_config* cfg, int group, const void* k, const int64_t* k_stride_host,
+                         const void* v, const int64_t* v_stride_host, int n_tokens, const int32_t* pos,
+                         void* K4, void* V4, void* stream);
+
+/* Rows [first, first + count) of every sequence and KV head read back from
+ * the 4-bit caches into the same rows of K and V ([B][H_kv][n_max][D],
+ * kv_dtype; either may be null): middle + scale * code in 32 bits, rounded
+ * to the cache's type.  The rows must have been written (or the buffer
+ * cleared: zero bytes read back as zeros).
+ * Errors: CKV_ERR_INVALID_ARG, CKV_ERR_CUDA. */
+ckv_status ckv_kv4_read(const ckv_config* cfg, int group, const void* K4, const void* V4, int first, int count,
+                        void* K, void* V, void* stream);
+
+/* Scratch of the two calls below: bytes of device memory, cleared to zero
+ * once before its first use and left ready for the next call by each call.
+ * Calls that may run at the same time (two streams, two graphs replayed at
+ * once) need a workspace each. */
+size_t ckv_kv4_workspace(const ckv_config* cfg);           /* 0 for a bad argument */
+
+/* Dense decode attention over 4-bit caches, ckv_dense_decode's counterpart:
+ * every query head attends over the positions [0, len_b) of its KV head,
+ * out = softmax(q K^T / sqrt(D)) V and lse = m + ln(l).  len_b = lens[b]
+ * (device [B], clamped to [0, n]) or n for every sequence where lens is
+ * null; a sequence of no positions gives out 0 and lse -infinity.  Rows at or
+ * behind len_b are never used.  q [B][H_q][D] (kv_dtype), out [B][H_q][D] and
+ * lse [B][H_q] (may be null) float32, device.  The logits are formed from q
+ * as 28-bit fixed point of its head's largest channel.  Supported for
+ * H_q / H_kv <= 8.
+ * Errors: CKV_ERR_INVALID_ARG (also n outside [1, n_max]), CKV_ERR_CUDA. */
+ckv_status ckv_kv4_dense_decode(const ckv_config* cfg, int group, const void* q, const void* K4, const void* V4,
+                                int n, const int32_t* lens, void* workspace, float* out, float* lse, void* stream);
+
+/* Sparse decode attention over chosen rows of 4-bit caches, the counterpart
+ * of ckv_attend_rows_static: for every graph g of cfg->mode (one per query
+ * head or one per KV head), its query heads attend over the sinks
+ * [0, n_sinks), the positions rows[g][0 .. n_rows[g]) and the new token
+ * len_b - 1 (lens and n as above).  rows [G][max_rows] and n_rows [G] are
+ * device memory.  An entry outside [n_sinks, len_b - 1) is no row (-1 pads a
+ * list); a row listed twice counts twice; n_rows is clamped to
+ * [0, max_rows].  A sequence of len_b <= n_sinks positions attends to those.
+ * Errors: as ckv_kv4_dense_decode. */
+ckv_status ckv_kv4_attend_rows(const ckv_config* cfg, int group, const void* q, const void* K4, const void* V4,
+                               int n, const int32_t* lens, const int32_t* rows, const int32_t* n_rows, int max_rows,
+                               void* workspace, float* out, float* lse, void* stream);
+
 /* Auxiliary storage of the context (centroids, community index, member
  * pool, decode-time edges; scratch excluded) and, for comparison, the bytes
  * of the K and V caches it serves. */

@@ -38,6 +38,15 @@ class ckv_config(ctypes.Structure):
         "n_sinks", "kappa", "budget", "slack", "kv_dtype", "mode", "device", "pool_capacity")]
 
 
+class ckv_qkv(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("n_tokens", "rot_dim", "interleaved", "group")] + \
+        [("eps", ctypes.c_float), ("rot_scale", ctypes.c_float)] + \
+        [(name, ctypes.c_void_p) for name in ("inv_freq_host", "q", "k", "v")] + \
+        [(name, ctypes.c_int64 * 3) for name in ("q_stride", "k_stride", "v_stride")] + \
+        [(name, ctypes.c_void_p) for name in ("pos", "q_weight", "k_weight", "q_out")] + \
+        [("q_out_stride", ctypes.c_int64 * 3)] + [(name, ctypes.c_void_p) for name in ("K", "V", "K4", "V4")]
+
+
 class CkvError(RuntimeError):
     def __init__(self, call: str, status: int):
         self.status = status
@@ -119,6 +128,21 @@ def lib() -> ctypes.CDLL:
     L.ckv_step_recall.argtypes = [P, P, P, I, P, P]
     L.ckv_dense_decode.restype = st
     L.ckv_dense_decode.argtypes = [P, P, P, P, I, P, P, P]
+    C = ctypes.POINTER(ckv_config)
+    L.ckv_kv4_bytes.restype = sz
+    L.ckv_kv4_bytes.argtypes = [C, I]
+    L.ckv_kv4_workspace.restype = sz
+    L.ckv_kv4_workspace.argtypes = [C]
+    L.ckv_qk_norm_rope.restype = st
+    L.ckv_qk_norm_rope.argtypes = [C, ctypes.POINTER(ckv_qkv), P]
+    L.ckv_kv4_write.restype = st
+    L.ckv_kv4_write.argtypes = [C, I, P, P, P, P, I, P, P, P, P]
+    L.ckv_kv4_read.restype = st
+    L.ckv_kv4_read.argtypes = [C, I, P, P, I, I, P, P, P]
+    L.ckv_kv4_dense_decode.restype = st
+    L.ckv_kv4_dense_decode.argtypes = [C, I, P, P, P, I, P, P, P, P, P]
+    L.ckv_kv4_attend_rows.restype = st
+    L.ckv_kv4_attend_rows.argtypes = [C, I, P, P, P, I, P, P, P, I, P, P, P, P]
     L.ckv_status_string.restype = ctypes.c_char_p
     L.ckv_status_string.argtypes = [I]
     _lib = L
@@ -354,6 +378,145 @@ def ckv_dense_decode(ctx, q, K, V, n, out, lse=None, stream=None):
     """Dense decode attention over [0, n): out [B][H_q][D], lse [B][H_q] (optional)."""
     _check("ckv_dense_decode", lib().ckv_dense_decode(ctx, _dev(q), _dev(K), _dev(V), n, _dev(out), _dev(lse),
                                                       _stream(stream)))
+
+
+# ----------------------------------------- rows into the caches, 4-bit caches
+_I3 = ctypes.c_int64 * 3
+
+
+def _dtypes():
+    """torch's (int32, float32, {kv_dtype: element type}); torch is imported by whoever holds its tensors."""
+    global _dtypes_known
+    if _dtypes_known is None:
+        import torch
+        _dtypes_known = torch.int32, torch.float32, {CKV_F32: torch.float32, CKV_BF16: torch.bfloat16}
+    return _dtypes_known
+
+
+_dtypes_known = None
+
+
+def _refuse(what, device, x):
+    _dev(x)                                                        # host memory: TypeError
+    raise ValueError(f"expected {what} on device {device}, got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on "
+                     f"{x.device}")
+
+
+def _on(device, x, dtype, shape):
+    """Address of a device argument: a contiguous tensor of `dtype` and
+    `shape` on `device`, a raw int address or None."""
+    if x is None or x.__class__ is int:
+        return x
+    if not hasattr(x, "get_device") or x.get_device() != device or x.dtype is not dtype or x.shape != shape or \
+            not x.is_contiguous():
+        _refuse(f"a contiguous {dtype} tensor of shape {tuple(shape)}", device, x)
+    return x.data_ptr()
+
+
+def _buffer(device, x, size):
+    """Address of a byte buffer (a 4-bit cache, a workspace) of at least `size` bytes."""
+    if x is None or x.__class__ is int:
+        return x
+    if not hasattr(x, "get_device") or x.get_device() != device or x.numel() * x.element_size() < size or \
+            not x.is_contiguous():
+        _refuse(f"a contiguous buffer of {size} bytes", device, x)
+    return x.data_ptr()
+
+
+def _rows4(device, x, dtype, shape):
+    """Address and (batch, token, head) strides of rows [B][T][heads][D]: a
+    CUDA tensor of that shape, its channels contiguous."""
+    if not hasattr(x, "get_device") or x.get_device() != device or x.dtype is not dtype or x.shape != shape:
+        if x is None or isinstance(x, int):
+            raise TypeError("expected a CUDA tensor of rows")
+        _refuse(f"{dtype} rows of shape {tuple(shape)}", device, x)
+    batch, token, head, channel = x.stride()
+    if channel != 1:
+        _refuse(f"{dtype} rows with contiguous channels", device, x)
+    return x.data_ptr(), _I3(batch, token, head)
+
+
+def ckv_kv4_bytes(cfg, group) -> int:
+    return lib().ckv_kv4_bytes(ctypes.byref(cfg), group)
+
+
+def ckv_kv4_workspace(cfg) -> int:
+    return lib().ckv_kv4_workspace(ctypes.byref(cfg))
+
+
+def ckv_qk_norm_rope(cfg, q, k, v, pos, q_out, inv_freq_host, *, q_weight=None, k_weight=None, eps=1e-6, rot_scale=1.0,
+                     interleaved=False, K=None, V=None, K4=None, V4=None, group=0, stream=None):
+    """Norm and rotation of q and k, rows into the caches.  q, k, v, q_out are
+    CUDA tensors [B][T][heads][D] with any (batch, token, head) strides;
+    inv_freq_host is a host array of rot_dim / 2 float64 frequencies (None: no
+    rotation)."""
+    L, (i32, _, elems) = lib(), _dtypes()
+    B, Hq, Hkv, D, dev = cfg.batch, cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.device
+    elem = elems[cfg.kv_dtype]
+    T = k.shape[1]
+    rot, freq = 0, None
+    if inv_freq_host is not None:
+        freq, rot = _hostp(inv_freq_host), 2 * len(inv_freq_host)
+        if str(inv_freq_host.dtype)[-7:] != "float64" or inv_freq_host.ndim != 1 or \
+                not (inv_freq_host.is_contiguous() if hasattr(inv_freq_host, "is_contiguous")
+                     else inv_freq_host.flags["C_CONTIGUOUS"]):
+            raise TypeError("expected a contiguous float64 array of frequencies")
+    qp, qs = _rows4(dev, q, elem, (B, T, Hq, D))
+    kp, ks = _rows4(dev, k, elem, (B, T, Hkv, D))
+    vp, vs = _rows4(dev, v, elem, (B, T, Hkv, D))
+    op, os_ = _rows4(dev, q_out, elem, (B, T, Hq, D))
+    cache = (B, Hkv, cfg.n_max, D)
+    size = L.ckv_kv4_bytes(ctypes.byref(cfg), group) if K4 is not None or V4 is not None else 0
+    x = ckv_qkv(T, rot, bool(interleaved), group, eps, rot_scale, freq, qp, kp, vp, qs, ks, vs, _on(dev, pos, i32, (B, T)),
+                _on(dev, q_weight, elem, (D,)), _on(dev, k_weight, elem, (D,)), op, os_, _on(dev, K, elem, cache),
+                _on(dev, V, elem, cache), _buffer(dev, K4, size), _buffer(dev, V4, size))
+    _check("ckv_qk_norm_rope", L.ckv_qk_norm_rope(ctypes.byref(cfg), ctypes.byref(x), _stream(stream)))
+
+
+def ckv_kv4_write(cfg, group, k, v, pos, K4, V4, stream=None):
+    """Rows k, v (CUDA tensors [B][T][H_kv][D], any strides) into the 4-bit
+    caches at pos [B][T] (None: 0 .. T-1)."""
+    L, (i32, _, elems), c = lib(), _dtypes(), ctypes.byref(cfg)
+    dev, T, elem = cfg.device, k.shape[1], elems[cfg.kv_dtype]
+    shape = (cfg.batch, T, cfg.n_kv_heads, cfg.head_dim)
+    kp, ks = _rows4(dev, k, elem, shape)
+    vp, vs = _rows4(dev, v, elem, shape)
+    size = L.ckv_kv4_bytes(c, group)
+    _check("ckv_kv4_write", L.ckv_kv4_write(c, group, kp, ks, vp, vs, T, _on(dev, pos, i32, shape[:2]),
+                                            _buffer(dev, K4, size), _buffer(dev, V4, size), _stream(stream)))
+
+
+def ckv_kv4_read(cfg, group, K4, V4, first, count, K, V, stream=None):
+    """Rows [first, first + count) of the 4-bit caches into the same rows of K and V."""
+    L, c, dev, elem = lib(), ctypes.byref(cfg), cfg.device, _dtypes()[2][cfg.kv_dtype]
+    size = L.ckv_kv4_bytes(c, group)
+    cache = (cfg.batch, cfg.n_kv_heads, cfg.n_max, cfg.head_dim)
+    _check("ckv_kv4_read", L.ckv_kv4_read(c, group, _buffer(dev, K4, size), _buffer(dev, V4, size), first, count,
+                                          _on(dev, K, elem, cache), _on(dev, V, elem, cache), _stream(stream)))
+
+
+def ckv_kv4_dense_decode(cfg, group, q, K4, V4, n, lens, workspace, out, lse=None, stream=None):
+    """Dense decode attention over 4-bit caches: positions [0, lens[b]) (None: [0, n))."""
+    L, (i32, f32, elems), c = lib(), _dtypes(), ctypes.byref(cfg)
+    dev, heads = cfg.device, (cfg.batch, cfg.n_q_heads)
+    rows, size = heads + (cfg.head_dim,), L.ckv_kv4_bytes(c, group)
+    _check("ckv_kv4_dense_decode", L.ckv_kv4_dense_decode(
+        c, group, _on(dev, q, elems[cfg.kv_dtype], rows), _buffer(dev, K4, size), _buffer(dev, V4, size), n,
+        _on(dev, lens, i32, heads[:1]), _buffer(dev, workspace, L.ckv_kv4_workspace(c)), _on(dev, out, f32, rows),
+        _on(dev, lse, f32, heads), _stream(stream)))
+
+
+def ckv_kv4_attend_rows(cfg, group, q, K4, V4, n, lens, rows, n_rows, max_rows, workspace, out, lse=None, stream=None):
+    """Decode attention over the sinks, rows[g][0 .. n_rows[g]) and the new token of 4-bit caches."""
+    L, (i32, f32, elems), c = lib(), _dtypes(), ctypes.byref(cfg)
+    dev, heads = cfg.device, (cfg.batch, cfg.n_q_heads)
+    shape, size = heads + (cfg.head_dim,), L.ckv_kv4_bytes(c, group)
+    graphs = cfg.batch * (cfg.n_q_heads if cfg.mode == CKV_PER_HEAD else cfg.n_kv_heads)
+    _check("ckv_kv4_attend_rows", L.ckv_kv4_attend_rows(
+        c, group, _on(dev, q, elems[cfg.kv_dtype], shape), _buffer(dev, K4, size), _buffer(dev, V4, size), n,
+        _on(dev, lens, i32, heads[:1]), _on(dev, rows, i32, (graphs, max_rows)), _on(dev, n_rows, i32, (graphs,)),
+        max_rows, _buffer(dev, workspace, L.ckv_kv4_workspace(c)), _on(dev, out, f32, shape), _on(dev, lse, f32, heads),
+        _stream(stream)))
 
 
 def ckv_debug_poke(ctx, what: int, g: int, c: int, r: int, value: int):

@@ -26,6 +26,7 @@
 #include <mutex>
 
 #include "ckv_internal.cuh"
+#include "device_guard.h"
 
 #define CKV_API extern "C" __attribute__((visibility("default")))
 
@@ -44,22 +45,6 @@ std::mutex g_setup_mutex;
 DeviceSetup g_setup[kMaxDevices];
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Restores the caller's current device when the call returns.
-struct DeviceGuard {
-    int prev = -1;
-    cudaError_t enter(int dev)
-    {
-        cudaError_t e = cudaGetDevice(&prev);
-        if (e != cudaSuccess) { prev = -1; return e; }
-        return prev == dev ? cudaSuccess : cudaSetDevice(dev);
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 }  // namespace
 
@@ -122,7 +107,7 @@ CKV_API ckv_status ckv_attend_rows_static(const ckv_config* cfg, const void* q, 
     const size_t o_po = off;    off = align256(off + (size_t)G * A * HG * kD * 4);
     if (off > kStaticScratchBytes) return CKV_ERR_CAPACITY;   // the rows and partials do not fit the array
 
-    DeviceGuard guard;
+    ckv::DeviceGuard guard;
     if (guard.enter(cfg->device) != cudaSuccess) return CKV_ERR_CUDA;
     DeviceSetup su;
     {
