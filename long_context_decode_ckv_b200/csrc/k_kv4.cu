@@ -6,15 +6,28 @@
 // the rows, out = sum_j p_j v_j, lse = m + ln(l).  With c the codes, s the
 // scales and m the middles of a row's groups G,
 //   q.k = sum_G s_G (q_G.c_G) + m_G sum(q_G),
-//   sum_j p_j v_j = sum_j (p_j s_jG) c_jG + sum_j p_j m_jG per group G.
+//   sum_j p_j v_j = sum_j (p_j s_jG) c_jG + sum_j p_j m_jG per group G,
+// so the codes go to the tensor cores as they are and the scales are applied
+// to 4 logits a lane, not to 128 channels a row.  Both products are exact but
+// for the rounding of their float operands and sums:
+//   q.c on the 8-bit integer MMA: q as 28-bit fixed point of its head's
+//     largest channel, four signed base-128 digits in the rows of A (4 heads x
+//     4 digits), a nibble in the high half of a byte as the code times 16;
+//     unpacking 8 codes takes 3 instructions and no conversion.
+//   (p s).c on the fp16 MMA: codes as fp16 integers, p s as two fp16 parts
+//     (22 bits) in the 8 columns of B (4 heads x 2 parts), times a power of
+//     two c_G that keeps the largest below 2^14.
 //
 // Work split: one unit per (batch, KV head), or per row list.  Units' tiles of
 // 16 rows are laid end to end and split evenly over the grid; a CTA's share
 // is one or more pieces (a run of one unit's tiles), and its warps take the
-// tiles of a piece in turn.  A piece's (m, l, o) per head goes to a slot of
-// its own; the unit's last piece to arrive merges the slots in their order,
-// so the result does not depend on which one that is.
+// tiles of a piece in turn, each through its own ring of cp.async stages.  A
+// piece's (m, l, o) per head goes to a slot of its own; the unit's last piece
+// to arrive merges the slots in their order, so the result does not depend on
+// which one that is.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -28,8 +41,10 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;                 // rows of a tile
+constexpr int kStages = 4;                // tiles of a warp's ring
 constexpr int kSlot = 2 + kD;             // slot row per head: m, l, o[D]
-constexpr float kScale = 0.08838834764831845f;   // 1 / sqrt(128)
+constexpr int kRed = kD + 2 + 4;          // a warp's result per head: o[D], m, l, the middles' sums
+constexpr double kLog2Scale = 0.08838834764831845 * 1.4426950408889634;   // log2(e) / sqrt(128)
 
 // what a unit attends to
 struct Unit {
@@ -80,97 +95,504 @@ __device__ __forceinline__ int owner_of(long long x, long long TT, int P)
     return (int)(((x + 1) * (long long)P - 1) / TT);
 }
 
-template <bool BF16>
-__device__ __forceinline__ float load_q(const void* q, int64_t i)
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const int (&c)[4])
 {
-    return BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]) : static_cast<const float*>(q)[i];
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%10,%11,%12,%13};\n"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]),
+                   "r"(c[3]));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// (lo, hi) -> fp16 pair, and an fp16 pair's halves
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// 4-bit codes of two rows, (x & mask) placed in an fp16 pair -> the codes.
+// Nibble n as 1024 + (n ^ 8) = 1032 + code, or 16 times higher up.
+__device__ __forceinline__ uint32_t codes_low(uint32_t x)
+{
+    const uint32_t u = (x & 0x000f000fu) ^ 0x64086408u, k = 0xe408e408u;   // -1032
+    const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&k));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t codes_high(uint32_t x)
+{
+    const uint32_t u = (x & 0x00f000f0u) ^ 0x64806480u, f = 0x2c002c00u, k = 0xd480d480u;   // 1/16, -72
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&f),
+                              *reinterpret_cast<const __half2*>(&k));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float middle_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <int N>
+struct Words {
+    uint32_t w[N];
+};
+template <int N>
+__device__ __forceinline__ Words<N> lds(const unsigned char* p)
+{
+    Words<N> r;
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r.w[0] = v.x; r.w[1] = v.y;
+    } else {
+        r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void* src)
+{
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 
-// One warp: rows of tiles t0 + warp, t0 + warp + kWarps, ... of [t0, t1); lane l holds channels 4 l .. 4 l + 3.
-template <bool BF16>
-__device__ __forceinline__ void warp_rows(const Kv4AttendArgs& a, const Unit& x, int u, int t0, int t1,
-                                          float (&m)[kKv4MaxHeads], float (&l)[kKv4MaxHeads],
-                                          float (&o)[kKv4MaxHeads][4])
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int NG = kD / a.group;
-    const int64_t base = ((int64_t)x.b * a.Hkv + x.kvh) * a.K4.R;
-    const int j = lane >> 3;
-    float q[kKv4MaxHeads][4];
-    for (int h = 0; h < kKv4MaxHeads; ++h)
-        for (int i = 0; i < 4; ++i)
-            q[h][i] = h < a.NH ? load_q<BF16>(a.q, ((int64_t)x.b * a.Hq + x.head0 + h) * kD + 4 * lane + i) : 0.f;
-    for (int tile = t0 + warp; tile < t1; tile += kWarps)
-        for (int e = tile * kTile; e < tile * kTile + kTile; ++e) {
-            const int row = entry_row(a, x, u, e);
-            if (row < 0) continue;
-            const int64_t at = base + row;
-            // K: channels 32 j + 8 t + 4 h + i at bytes 16 t + 4 j + i
-            const int t = (lane & 7) >> 1, hi = lane & 1;
-            const uint32_t kw = *reinterpret_cast<const uint32_t*>(a.K4.codes + at * kRowCodes + 16 * t + 4 * j) >> (4 * hi);
-            const uint32_t vw = *reinterpret_cast<const uint16_t*>(a.V4.codes + at * kRowCodes + 8 * (lane & 7) + 2 * j);
-            const uint32_t kp = a.K4.params[at * NG + 4 * lane / a.group], vp = a.V4.params[at * NG + 4 * lane / a.group];
-            float k[4], v[4];
-            for (int i = 0; i < 4; ++i) {
-                k[i] = fmaf(__uint_as_float(kp << 16), (float)((int)(kw << (28 - 8 * i)) >> 28), __uint_as_float(kp & 0xffff0000u));
-                v[i] = fmaf(__uint_as_float(vp << 16), (float)((int)(vw << (28 - 4 * i)) >> 28), __uint_as_float(vp & 0xffff0000u));
+// One stage of a warp's ring: 16 rows of K codes, V codes, K parameters, V
+// parameters and the rows' mask.  V's 16-byte chunks of rows 4-7 and 12-15
+// are swapped by halves, so that the 8-byte reads of four rows that a half
+// warp makes at once fall into different banks.
+template <int NG>
+struct Stage {
+    static constexpr int K = 0, V = 1024, KP = 2048, VP = KP + 64 * NG, MASK = VP + 64 * NG, bytes = MASK + 16;
+};
+template <int NG>
+constexpr int kSmem = kWarps * kStages * Stage<NG>::bytes;
+
+// NG: groups of a row.  NT: blocks of 4 query heads.  A lane is (g, t) =
+// (lane / 4, lane % 4).
+template <int NG, int NT>
+struct Warp {
+    static constexpr int NGH = NG > 1 ? NG / 2 : 1;    // groups whose middles this lane's half (g / 4) sums
+
+    uint32_t qa[NT][4][4];   // digits of q: A of the k32 step j
+    float qs[NT][NGH];       // sum of q over a group, in units of the lane's integer logit
+    float F[NT];             // logit (in powers of two) of one such unit
+    float m[NT], l[NT];      // running maximum and this lane's share of the sum, head 4 nt + g % 4
+    float Z[NT][NGH];        // this lane's share of sum p * middle
+    float acc[NT][8][4];     // sum (p s c_G) code: [channel block J, pair of channels][..]
+    float c[NG];
+    uint32_t top[2];         // largest scale bits that c allows, of the groups this lane watches
+
+    // ---- the unit's queries
+    __device__ __forceinline__ void start(const Kv4AttendArgs& a, const Unit& x, bool bf16)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = 4 * nt + (g & 3);
+            float q[4][8];
+            float top_q = 0.f, nan = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t at = ((int64_t)x.b * a.Hq + x.head0 + h) * kD + 32 * j + 8 * t;
+                if (h >= a.NH) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[j][i] = 0.f;
+                } else if (bf16) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) { q[j][2 * i] = bf_lo(w[i]); q[j][2 * i + 1] = bf_hi(w[i]); }
+                } else {
+                    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+                    const float4 u = p[0], v = p[1];
+                    q[j][0] = u.x; q[j][1] = u.y; q[j][2] = u.z; q[j][3] = u.w;
+                    q[j][4] = v.x; q[j][5] = v.y; q[j][6] = v.z; q[j][7] = v.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    top_q = fmaxf(top_q, fabsf(q[j][i]));
+                    nan = fmaf(q[j][i], 0.f, nan);
+                }
             }
-            for (int h = 0; h < a.NH; ++h) {
-                float z = q[h][0] * k[0] + q[h][1] * k[1] + q[h][2] * k[2] + q[h][3] * k[3];
-                for (int off = 16; off; off >>= 1) z += __shfl_xor_sync(kFull, z, off);
-                z *= kScale;
-                const float mn = fmaxf(m[h], z);
-                const float al = m[h] == -INFINITY ? 0.f : expf(m[h] - mn), p = expf(z - mn);
-                l[h] = l[h] * al + p;
-                for (int i = 0; i < 4; ++i) o[h][i] = o[h][i] * al + p * v[i];
-                m[h] = mn;
+#pragma unroll
+            for (int off = 1; off <= 2; off <<= 1) {
+                top_q = fmaxf(top_q, __shfl_xor_sync(kFull, top_q, off));
+                nan += __shfl_xor_sync(kFull, nan, off);
+            }
+            const bool bad = nan != 0.f;                       // an infinity or a NaN in the head
+            if (bad) top_q = 0.f;
+            // |q| < 2^e; q = X 2^(e - 27)
+            const int e = top_q > 0.f ? (int)((__double_as_longlong((double)top_q) >> 52) & 2047) - 1022 : 0;
+            const double to_fixed = __longlong_as_double((long long)(1023 + 27 - e) << 52);
+            const double unit = __longlong_as_double((long long)(1023 + e - 27) << 52);
+            long long sum[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t d[4] = {0u, 0u, 0u, 0u};              // [channels 4..7 / 0..3 of 8 t ..][first / second digit]
+                int part = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int X = bad ? 0 : __double2int_rn((double)q[j][i] * to_fixed);
+                    part += X;                                 // 8 * 2^27 at most
+                    const int d3 = ((X + 64) & 127) - 64, X1 = (X - d3) >> 7;
+                    const int d2 = ((X1 + 64) & 127) - 64, X2 = (X1 - d2) >> 7;
+                    const int d1 = ((X2 + 64) & 127) - 64, d0 = (X2 - d1) >> 7;
+                    const int hi = g < 4 ? d0 : d2, lo = g < 4 ? d1 : d3;
+                    d[i < 4 ? 2 : 0] |= (uint32_t)(hi & 255) << (8 * (i & 3));
+                    d[i < 4 ? 3 : 1] |= (uint32_t)(lo & 255) << (8 * (i & 3));
+                }
+                // rows g and g + 8 of A: the lane half's first and second digit
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qa[nt][j][i] = d[i];
+                sum[j] = part;
+                sum[j] += __shfl_xor_sync(kFull, sum[j], 1);
+                sum[j] += __shfl_xor_sync(kFull, sum[j], 2);
+            }
+            // a lane's integer logit counts units of 2^14 (first half) or 1, times 16 (the codes)
+            const double in_units = (g < 4 ? 1.0 / 16384.0 : 1.0) * 16.0;
+            if constexpr (NG == 4) {
+                qs[nt][0] = (float)((double)(g < 4 ? sum[0] : sum[2]) * in_units);
+                qs[nt][1] = (float)((double)(g < 4 ? sum[1] : sum[3]) * in_units);
+            } else if constexpr (NG == 2) {
+                qs[nt][0] = (float)((double)(g < 4 ? sum[0] + sum[1] : sum[2] + sum[3]) * in_units);
+            } else {
+                qs[nt][0] = (float)((double)(sum[0] + sum[1] + sum[2] + sum[3]) * 0.5 * in_units);
+            }
+            F[nt] = bad ? NAN : (float)(unit * kLog2Scale * (g < 4 ? 1024.0 : 0.0625));
+            m[nt] = -FLT_MAX;
+            l[nt] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NGH; ++j) Z[nt][j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[nt][i][r] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) c[j] = 1.2676506e30f;     // 2^100: scales below 2^-86
+        top[0] = top[1] = ((uint32_t)(127 - 86) << 23) - 1u;
+    }
+
+    // ---- larger value scales than so far: c_G down, sums with it
+    __device__ __forceinline__ void raise(uint32_t w0, uint32_t w1)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            uint32_t v = 0u;
+            if (NG == 4) v = (lane & 1) == (j >> 1) ? (j & 1 ? w1 : w0) << 16 : 0u;
+            else if (NG == 2) v = (lane & 1) == j ? w0 << 16 : 0u;
+            else v = w0 << 16;
+            const uint32_t most = __reduce_max_sync(kFull, v);
+            // scale < 2^e
+            int e = (int)((most >> 23) & 255u) - 126;
+            e = e < -86 ? -86 : e;
+            const float now = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            if (now < c[j]) {
+                const float f = now / c[j];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int J = 0; J < 4; ++J)
+                        if (J * NG / 4 == j)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) { acc[nt][2 * J][r] *= f; acc[nt][2 * J + 1][r] *= f; }
+                c[j] = now;
+                const uint32_t limit = ((uint32_t)(e + 127) << 23) - 1u;
+                if (NG == 4) { if ((lane & 1) == (j >> 1)) top[j & 1] = limit; }
+                else if (NG == 2) { if ((lane & 1) == j) top[0] = limit; }
+                else top[0] = limit;
             }
         }
-}
+    }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_kv4_attend(const __grid_constant__ Kv4AttendArgs a)
+    // ---- one tile; valid: its rows (bit = row of the tile)
+    __device__ __forceinline__ void tile(unsigned char* st, uint32_t valid)
+    {
+        using S = Stage<NG>;
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        // the rows of this lane's logits: columns 2 t and 2 t + 1 of the two
+        // MMAs; their order within the pair alternates with t (see Stage)
+        const int ra = 2 * t + (t & 1), rb = 2 * t + 1 - (t & 1);
+        const int rows[4] = {ra, rb, ra + 8, rb + 8};
+        if (valid != 0xffffu) {
+            // rows that are not there: their parameters may be anything
+            if (!((valid >> (lane & 15)) & 1u)) {
+                uint32_t* p = reinterpret_cast<uint32_t*>(st + (lane < 16 ? S::KP : S::VP)) + (lane & 15) * NG;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) p[j] = 0u;
+            }
+            __syncwarp();
+        }
+        // ---- logits
+        float z[NT][4];
+        {
+            float ks[4][NG], km[4][NGH];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Words<NG> w = lds<NG>(st + S::KP + rows[e] * (4 * NG));
+#pragma unroll
+                for (int j = 0; j < NG; ++j) ks[e][j] = scale_of(w.w[j]);
+                const Words<NGH> h = lds<NGH>(st + S::KP + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
+#pragma unroll
+                for (int j = 0; j < NGH; ++j) km[e][j] = middle_of(h.w[j]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z[nt][e] = km[e][0] * qs[nt][0];
+#pragma unroll
+                    for (int j = 1; j < NGH; ++j) z[nt][e] = fmaf(km[e][j], qs[nt][j], z[nt][e]);
+                }
+            // column n of MMA a is row 8 a + rowof(n): lane g loads that row
+            const int kr = 2 * (g >> 1) + ((g & 1) ^ ((g >> 1) & 1));
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const Words<4> w = lds<4>(st + S::K + (8 * a + kr) * kRowCodes + 16 * t);
+                int d[NT][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t b0 = w.w[j] & 0xf0f0f0f0u, b1 = (w.w[j] << 4) & 0xf0f0f0f0u;
+                    const int zero[4] = {0, 0, 0, 0};
+                    constexpr int per = 4 / NG;                // k32 steps of a group
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (j % per == 0) mma_s8(d[nt], qa[nt][j], b0, b1, zero);
+                        else mma_s8(d[nt], qa[nt][j], b0, b1, d[nt]);
+                        if (j % per == per - 1) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                z[nt][2 * a + i] = fmaf(ks[2 * a + i][j / per], (float)(d[nt][i] * 128 + d[nt][2 + i]),
+                                                        z[nt][2 * a + i]);
+                        }
+                    }
+                }
+            }
+        }
+        bool more = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                z[nt][e] *= F[nt];
+                z[nt][e] += __shfl_xor_sync(kFull, z[nt][e], 16);
+            }
+            if (valid != 0xffffu) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!((valid >> rows[e]) & 1u)) z[nt][e] = -INFINITY;
+            }
+            more |= fmaxf(fmaxf(z[nt][0], z[nt][1]), fmaxf(z[nt][2], z[nt][3])) > m[nt];
+        }
+        // ---- a new maximum: sums down
+        if (__any_sync(kFull, more)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float mx = fmaxf(fmaxf(z[nt][0], z[nt][1]), fmaxf(z[nt][2], z[nt][3]));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+                const float mn = fmaxf(m[nt], mx), f = ex2(m[nt] - mn);
+                m[nt] = mn;
+                l[nt] *= f;
+#pragma unroll
+                for (int j = 0; j < NGH; ++j) Z[nt][j] *= f;
+                // columns 2 t and 2 t + 1 of the sums: heads 2 t % 4 and + 1
+                const float f0 = __shfl_sync(kFull, f, ((2 * t) & 3) * 4), f1 = __shfl_sync(kFull, f, ((2 * t + 1) & 3) * 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    acc[nt][i][0] *= f0;
+                    acc[nt][i][2] *= f0;
+                    acc[nt][i][1] *= f1;
+                    acc[nt][i][3] *= f1;
+                }
+            }
+        }
+        // ---- larger scales among the values (each lane looks at two words of the parameters)
+        {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(st + S::VP);
+            const uint32_t w0 = NG == 4 ? p[2 * lane] : NG == 2 ? p[lane] : p[lane & 15], w1 = NG == 4 ? p[2 * lane + 1] : 0u;
+            if (__any_sync(kFull, (w0 << 16) > top[0] || (NG == 4 && (w1 << 16) > top[1]))) raise(w0, w1);
+        }
+        // ---- weights, and their products with the scales
+        uint32_t pb[NT][NG][2];
+        {
+            const float second = g < 4 ? 0.f : 1.f;            // this lane's column: first or second part
+            float p[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[nt][e] = ex2(z[nt][e] - m[nt]);
+                l[nt] += (p[nt][0] + p[nt][1]) + (p[nt][2] + p[nt][3]);
+            }
+            float vs[4][NG];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Words<NG> w = lds<NG>(st + S::VP + rows[e] * (4 * NG));
+#pragma unroll
+                for (int j = 0; j < NG; ++j) vs[e][j] = scale_of(w.w[j]) * c[j];
+                const Words<NGH> h = lds<NGH>(st + S::VP + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < NGH; ++j) Z[nt][j] = fmaf(p[nt][e], middle_of(h.w[j]), Z[nt][j]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float x0 = p[nt][2 * k] * vs[2 * k][j], x1 = p[nt][2 * k + 1] * vs[2 * k + 1][j];
+                        const float2 first = unpack_f16(pack_f16(x0, x1));
+                        pb[nt][j][k] = pack_f16(fmaf(-second, first.x, x0), fmaf(-second, first.y, x1));
+                    }
+        }
+        // ---- values: A is 16 channels x 16 rows
+        Words<2> v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = rows[e], chunk = (g >> 1) ^ ((r >> 1) & 2);
+            v[e] = lds<2>(st + S::V + r * kRowCodes + 16 * chunk + 8 * (g & 1));
+        }
+#pragma unroll
+        for (int J = 0; J < 4; ++J) {
+            const uint32_t sel = J & 1 ? 0x7632u : 0x5410u;
+            uint32_t x = __byte_perm(v[0].w[J >> 1], v[1].w[J >> 1], sel), y = __byte_perm(v[2].w[J >> 1], v[3].w[J >> 1], sel);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t a0 = codes_low(x), a1 = codes_high(x), a2 = codes_low(y), a3 = codes_high(y);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(acc[nt][2 * J + k], a0, a1, a2, a3, pb[nt][J * NG / 4][0], pb[nt][J * NG / 4][1]);
+                x >>= 8;
+                y >>= 8;
+            }
+        }
+    }
+
+    // ---- this warp's sums per head: o without the middles, m, l, the middles' sums
+    __device__ __forceinline__ void finish(float* red)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int J = 0; J < 4; ++J) {
+                const float inv = 1.f / c[J * NG / 4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float v = acc[nt][2 * J + k][r];
+                        v += __shfl_xor_sync(kFull, v, 2);     // first and second part
+                        if (t < 2) red[(4 * nt + 2 * t + (r & 1)) * kRed + 32 * J + 4 * g + 2 * k + (r >> 1)] = v * inv;
+                    }
+            }
+            float s = l[nt];
+            s += __shfl_xor_sync(kFull, s, 1);
+            s += __shfl_xor_sync(kFull, s, 2);
+            float* r = red + (4 * nt + (g & 3)) * kRed + kD;
+            if (t == 0 && g < 4) { r[0] = m[nt]; r[1] = s; }
+#pragma unroll
+            for (int j = 0; j < NGH; ++j) {
+                float v = Z[nt][j];
+                v += __shfl_xor_sync(kFull, v, 1);
+                v += __shfl_xor_sync(kFull, v, 2);
+                if (t == 0 && (NG > 1 || g < 4)) r[2 + (NG > 1 ? (g >> 2) * NGH : 0) + j] = v;
+            }
+        }
+    }
+};
+
+// weight of a part with maximum m and sum l in a merge with maximum M; a part without rows has l = 0
+__device__ __forceinline__ float part_weight(float m, float l, float M) { return l == 0.f ? 0.f : ex2(m - M); }
+
+// CTAs of an SM: two while a warp's sums fit 128 registers
+template <int NT>
+constexpr int kCtasPerSM = NT == 1 ? 2 : 1;
+
+template <int NG, int NT, bool ROWS>
+__global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const __grid_constant__ Kv4AttendArgs a, int bf16)
 {
-    __shared__ float red[kWarps][kSlot];
-    __shared__ long long s_scan[kThreads + 1];
+    using S = Stage<NG>;
+    static_assert(4 * NT * kRed * 4 <= kStages * S::bytes, "a warp's results must fit its ring");
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long s_scan[kWarps];
     __shared__ long long s_first[2];       // first unit of this CTA's share, tiles before that unit
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned char* ring = smem + warp * (kStages * S::bytes);
+    float* red = reinterpret_cast<float*>(smem);
+    constexpr int kRedWarp = kStages * S::bytes / 4;       // floats between two warps' results
     const int p = blockIdx.x;
 
     // ---- the share: tiles of all units, and the unit the share starts in
-    const int per = (a.U + kThreads - 1) / kThreads;
-    const int u0 = min(tid * per, a.U), u1 = min(u0 + per, a.U);
-    long long mine = 0;
-    for (int u = u0; u < u1; ++u) mine += tiles_of(unit_of(a, u).count);
-    s_scan[tid + 1] = mine;
-    if (tid == 0) s_scan[0] = 0;
-    __syncthreads();
-    if (tid == 0)
-        for (int i = 1; i <= kThreads; ++i) s_scan[i] += s_scan[i - 1];
-    __syncthreads();
-    const long long TT = s_scan[kThreads];
-    // no more shares than tiles: the arrivals of a unit count every CTA
-    // between its first and its last tile's owner
-    const int P = TT < gridDim.x ? (int)(TT > 0 ? TT : 1) : (int)gridDim.x;
-    const long long lo = p < P ? p * TT / P : TT, hi = p < P ? (p + 1) * TT / P : TT;
-    if (lo < hi && lo >= s_scan[tid] && lo < s_scan[tid + 1]) {
-        long long at = s_scan[tid];
-        int u = u0;
-        for (;; ++u) {
-            const int n = tiles_of(unit_of(a, u).count);
-            if (lo < at + n) break;
-            at += n;
+    long long TT;
+    int P;
+    long long lo, hi;
+    if (!ROWS && !a.lens) {
+        const long long per = tiles_of(a.n);
+        TT = per * a.U;
+        P = TT < gridDim.x ? (int)TT : (int)gridDim.x;
+        lo = p < P ? p * TT / P : TT;
+        hi = p < P ? (p + 1) * TT / P : TT;
+        if (tid == 0) { s_first[0] = lo / per; s_first[1] = lo / per * per; }
+    } else {
+        const int per = (a.U + kThreads - 1) / kThreads;
+        const int u0 = min(tid * per, a.U), u1 = min(u0 + per, a.U);
+        long long mine = 0;
+        for (int u = u0; u < u1; ++u) mine += tiles_of(unit_of(a, u).count);
+        long long upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(kFull, upto, off);
+            if (lane >= off) upto += o;
         }
-        s_first[0] = u;
-        s_first[1] = at;
-    }
-    // units with nothing to attend to: 0 and -inf
-    for (int u = p; u < a.U; u += gridDim.x) {
-        const Unit x = unit_of(a, u);
-        if (x.count) continue;
-        for (int i = tid; i < a.NH * kD; i += kThreads) a.out[((int64_t)x.b * a.Hq + x.head0) * kD + i] = 0.f;
-        if (a.lse && tid < a.NH) a.lse[(int64_t)x.b * a.Hq + x.head0 + tid] = -INFINITY;
+        if (lane == 31) s_scan[warp] = upto;
+        __syncthreads();
+        TT = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) upto += TT;
+            TT += s_scan[w];
+        }
+        // no more shares than tiles: the arrivals of a unit count every CTA
+        // between its first and its last tile's owner
+        P = TT < gridDim.x ? (int)(TT > 0 ? TT : 1) : (int)gridDim.x;
+        lo = p < P ? p * TT / P : TT;
+        hi = p < P ? (p + 1) * TT / P : TT;
+        if (lo < hi && lo >= upto - mine && lo < upto) {
+            long long at = upto - mine;
+            int u = u0;
+            for (;; ++u) {
+                const int n = tiles_of(unit_of(a, u).count);
+                if (lo < at + n) break;
+                at += n;
+            }
+            s_first[0] = u;
+            s_first[1] = at;
+        }
+        // units with nothing to attend to: 0 and -inf
+        for (int u = p; u < a.U; u += gridDim.x) {
+            const Unit x = unit_of(a, u);
+            if (x.count) continue;
+            for (int i = tid; i < a.NH * kD; i += kThreads) a.out[((int64_t)x.b * a.Hq + x.head0) * kD + i] = 0.f;
+            if (a.lse && tid < a.NH) a.lse[(int64_t)x.b * a.Hq + x.head0 + tid] = -INFINITY;
+        }
     }
     __syncthreads();
     if (lo >= hi) return;
@@ -183,30 +605,92 @@ __global__ void __launch_bounds__(kThreads) k_kv4_attend(const __grid_constant__
         const long long end = before + tiles_of(x.count);
         if (end == before) continue;
         const int t0 = (int)(at - before), t1 = (int)((hi < end ? hi : end) - before);
-        float m[kKv4MaxHeads], l[kKv4MaxHeads], o[kKv4MaxHeads][4];
-        for (int h = 0; h < kKv4MaxHeads; ++h) {
-            m[h] = -INFINITY;
-            l[h] = 0.f;
-            for (int i = 0; i < 4; ++i) o[h][i] = 0.f;
-        }
-        warp_rows<BF16>(a, x, u, t0, t1, m, l, o);
-        float* slot = a.part + (int64_t)(u + p) * a.NH * kSlot;
-        for (int h = 0; h < a.NH; ++h) {
-            __syncthreads();
-            if (lane == 0) { red[warp][0] = m[h]; red[warp][1] = l[h]; }
-            for (int i = 0; i < 4; ++i) red[warp][2 + 4 * lane + i] = o[h][i];
-            __syncthreads();
-            if (tid < kD) {
-                float M = -INFINITY, L = 0.f, O = 0.f;
-                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[w][0]);
-                for (int w = 0; w < kWarps; ++w) {
-                    const float c = red[w][0] == -INFINITY ? (red[w][1] == 0.f ? 0.f : 1.f) : expf(red[w][0] - M);
-                    L += c * red[w][1];
-                    O += c * red[w][2 + tid];
+        {
+            const int first = t0 + warp;
+            const int nb = t1 > first ? (t1 - first + kWarps - 1) / kWarps : 0;
+            const int64_t row0 = ((int64_t)x.b * a.Hkv + x.kvh) * a.K4.R;
+            const unsigned char* kc = a.K4.codes + row0 * kRowCodes;
+            const unsigned char* vc = a.V4.codes + row0 * kRowCodes;
+            const uint32_t* par = (lane < 16 ? a.K4.params : a.V4.params) + row0 * NG;
+            const uint32_t ring_at = smem_u32(ring);
+            const int r8 = lane >> 2, ch = lane & 3;
+            // entry (lane % 16) of the warp's tile i: its position, -1 for none
+            auto entry = [&](int i) { return i < nb ? entry_row(a, x, u, (first + i * kWarps) * kTile + (lane & 15)) : -1; };
+            auto issue = [&](int i, int row) {
+                if (i < nb) {
+                    const uint32_t st = ring_at + (i % kStages) * S::bytes;
+                    int k0, k1, pr;
+                    if (ROWS) {
+                        const uint32_t mask = __ballot_sync(kFull, row >= 0) & 0xffffu;
+                        row = max(row, 0);
+                        k0 = __shfl_sync(kFull, row, r8);
+                        k1 = __shfl_sync(kFull, row, r8 + 8);
+                        pr = row;
+                        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + (i % kStages) * S::bytes + S::MASK) = mask;
+                    } else {
+                        const int base = (first + i * kWarps) * kTile;   // the cache's rows are padded to whole tiles
+                        k0 = base + r8;
+                        k1 = k0 + 8;
+                        pr = base + (lane & 15);
+                    }
+                    const int sw = (r8 >> 1) & 2;
+                    cp_async_bytes<16>(st + S::K + r8 * kRowCodes + 16 * ch, kc + (int64_t)k0 * kRowCodes + 16 * ch);
+                    cp_async_bytes<16>(st + S::K + (r8 + 8) * kRowCodes + 16 * ch, kc + (int64_t)k1 * kRowCodes + 16 * ch);
+                    cp_async_bytes<16>(st + S::V + r8 * kRowCodes + 16 * (ch ^ sw), vc + (int64_t)k0 * kRowCodes + 16 * ch);
+                    cp_async_bytes<16>(st + S::V + (r8 + 8) * kRowCodes + 16 * (ch ^ sw), vc + (int64_t)k1 * kRowCodes + 16 * ch);
+                    cp_async_bytes<4 * NG>(st + S::KP + lane * (4 * NG), par + (int64_t)pr * NG);
                 }
-                slot[h * kSlot + 2 + tid] = O;
-                if (tid == 0) { slot[h * kSlot] = M; slot[h * kSlot + 1] = L; }
+                cp_async_commit();
+            };
+            int row = 0;
+            if (ROWS) row = entry(0);
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) {
+                const int now = row;
+                if (ROWS) row = entry(i + 1);
+                issue(i, now);
             }
+            Warp<NG, NT> w;
+            w.start(a, x, bf16 != 0);
+            for (int i = 0; i < nb; ++i) {
+                const int now = row;
+                if (ROWS) row = entry(i + kStages);
+                issue(i + kStages - 1, now);
+                cp_async_wait<kStages - 1>();
+                __syncwarp();
+                unsigned char* st = ring + (i % kStages) * S::bytes;
+                uint32_t valid = 0xffffu;
+                if (ROWS) {
+                    valid = *reinterpret_cast<const uint32_t*>(st + S::MASK);
+                } else {
+                    const int left = x.count - (first + i * kWarps) * kTile;
+                    if (left < kTile) valid = (1u << left) - 1u;
+                }
+                w.tile(st, valid);
+                __syncwarp();
+            }
+            cp_async_wait<0>();
+            __syncwarp();
+            w.finish(reinterpret_cast<float*>(ring));          // the ring is drained
+        }
+        __syncthreads();
+        // ---- the piece's slot: the warps merged per head
+        float* slot = a.part + (int64_t)(u + p) * a.NH * kSlot;
+        for (int i = tid; i < a.NH * kD; i += kThreads) {
+            const int h = i / kD, d = i % kD;
+            const float* r = red + h * kRed;
+            float M = -FLT_MAX, L = 0.f, O = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, r[w * kRedWarp + kD]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float* rw = r + w * kRedWarp;
+                const float f = part_weight(rw[kD], rw[kD + 1], M);
+                L += f * rw[kD + 1];
+                O += f * (rw[d] + rw[kD + 2 + d * NG / kD]);
+            }
+            slot[h * kSlot + 2 + d] = O;
+            if (d == 0) { slot[h * kSlot] = M; slot[h * kSlot + 1] = L; }
         }
         __threadfence();
         __syncthreads();
@@ -219,38 +703,60 @@ __global__ void __launch_bounds__(kThreads) k_kv4_attend(const __grid_constant__
             const float* s0 = a.part + (int64_t)(u + pf) * a.NH * kSlot;
             for (int i = tid; i < a.NH * kD; i += kThreads) {
                 const int h = i / kD, d = i % kD;
-                float M = -INFINITY, L = 0.f, O = 0.f;
+                float M = -FLT_MAX, L = 0.f, O = 0.f;
                 for (int s = 0; s <= pl - pf; ++s) M = fmaxf(M, __ldcg(s0 + ((int64_t)s * a.NH + h) * kSlot));
                 for (int s = 0; s <= pl - pf; ++s) {
                     const float* q = s0 + ((int64_t)s * a.NH + h) * kSlot;
-                    const float ms = __ldcg(q), ls = __ldcg(q + 1);
-                    const float c = ms == -INFINITY ? (ls == 0.f ? 0.f : 1.f) : expf(ms - M);
-                    L += c * ls;
-                    O += c * __ldcg(q + 2 + d);
+                    const float ls = __ldcg(q + 1);
+                    const float f = part_weight(__ldcg(q), ls, M);
+                    L += f * ls;
+                    O += f * __ldcg(q + 2 + d);
                 }
                 const int64_t hq = (int64_t)x.b * a.Hq + x.head0 + h;
                 a.out[hq * kD + d] = L == 0.f ? 0.f : O / L;
-                if (d == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : M + logf(L);
+                if (d == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
             }
             if (tid == 0) a.cnt[u] = 0;
         }
+        __syncthreads();   // the rings are written again by the next piece
         at = before + t1;
         before = end;
     }
+}
+
+template <int NG, int NT, bool ROWS>
+cudaError_t launch_attend_t(const Kv4AttendArgs& a, int bf16, int sms, cudaStream_t st)
+{
+    auto fn = k_kv4_attend<NG, NT, ROWS>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<NG>);
+    if (e != cudaSuccess) return e;
+    long long tiles = ROWS ? ((long long)a.S + a.max_rows + 1 + kTile - 1) / kTile : (a.n + kTile - 1) / kTile;
+    tiles *= a.U;
+    long long P = (tiles + kWarps - 1) / kWarps;
+    P = P < (long long)kCtasPerSM<NT> * sms ? P : (long long)kCtasPerSM<NT> * sms;
+    P = P < kKv4MaxCtas ? P : kKv4MaxCtas;
+    fn<<<(unsigned)P, kThreads, kSmem<NG>, st>>>(a, bf16);
+    return cudaGetLastError();
+}
+
+template <bool ROWS>
+cudaError_t launch_attend_g(const Kv4AttendArgs& a, int bf16, int sms, cudaStream_t st)
+{
+    if (a.NH <= 4) {
+        if (a.group == 32) return launch_attend_t<4, 1, ROWS>(a, bf16, sms, st);
+        if (a.group == 64) return launch_attend_t<2, 1, ROWS>(a, bf16, sms, st);
+        return launch_attend_t<1, 1, ROWS>(a, bf16, sms, st);
+    }
+    if (a.group == 32) return launch_attend_t<4, 2, ROWS>(a, bf16, sms, st);
+    if (a.group == 64) return launch_attend_t<2, 2, ROWS>(a, bf16, sms, st);
+    return launch_attend_t<1, 2, ROWS>(a, bf16, sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_attend(const Kv4AttendArgs& a, int bf16, int sms, cudaStream_t st)
 {
-    long long tiles = a.rows ? ((long long)a.S + a.max_rows + 1 + kTile - 1) / kTile : (a.n + kTile - 1) / kTile;
-    tiles *= a.U;
-    long long P = (tiles + kWarps - 1) / kWarps;
-    P = P < 4LL * sms ? P : 4LL * sms;
-    P = P < kKv4MaxCtas ? P : kKv4MaxCtas;
-    if (bf16) k_kv4_attend<true><<<(unsigned)P, kThreads, 0, st>>>(a);
-    else k_kv4_attend<false><<<(unsigned)P, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return a.rows ? launch_attend_g<true>(a, bf16, sms, st) : launch_attend_g<false>(a, bf16, sms, st);
 }
 
 }  // namespace ckv
