@@ -42,9 +42,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;                 // rows of a tile
 constexpr int kStages = 4;                // tiles of a warp's ring
-constexpr int kSlot = 2 + kD;             // slot row per head: m, l, o[D]
 constexpr int kRed = kD + 2 + 4;          // a warp's result per head: o[D], m, l, the middles' sums
-constexpr double kLog2Scale = 0.08838834764831845 * 1.4426950408889634;   // log2(e) / sqrt(128)
+constexpr float kLog2Scale = (float)(0.08838834764831845 * 1.4426950408889634);   // log2(e) / sqrt(128)
 
 // what a unit attends to
 struct Unit {
@@ -125,21 +124,26 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-// 4-bit codes of two rows, (x & mask) placed in an fp16 pair -> the codes.
-// Nibble n as 1024 + (n ^ 8) = 1032 + code, or 16 times higher up.
-__device__ __forceinline__ uint32_t codes_low(uint32_t x)
+// 4-bit codes of two rows (one per 16-bit half of x) as an fp16 pair: with
+// magic 0x6488 in both halves, a masked low nibble n becomes 1024 + 128 +
+// (n ^ 8) = 1160 + code, a high one 1024 + 16 (n ^ 8) + 8 = 16 (72.5 + code).
+__device__ __forceinline__ uint32_t codes_low(uint32_t x, uint32_t magic)
 {
-    const uint32_t u = (x & 0x000f000fu) ^ 0x64086408u, k = 0xe408e408u;   // -1032
+    const uint32_t u = (x & 0x000f000fu) ^ magic, k = 0xe488e488u;          // -1160
     const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&k));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t codes_high(uint32_t x)
+__device__ __forceinline__ uint32_t codes_high(uint32_t x, uint32_t magic, uint32_t offset)
 {
-    const uint32_t u = (x & 0x00f000f0u) ^ 0x64806480u, f = 0x2c002c00u, k = 0xd480d480u;   // 1/16, -72
+    const uint32_t u = (x & 0x00f000f0u) ^ magic, f = 0x2c002c00u;          // 1/16; offset: -72.5
     const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&f),
-                              *reinterpret_cast<const __half2*>(&k));
+                              *reinterpret_cast<const __half2*>(&offset));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+// a constant that stays in a register: an instruction takes one immediate,
+// and the compiler, which cannot see through the shuffle, would otherwise
+// rebuild the other one at every use
+__device__ __forceinline__ uint32_t held(uint32_t v) { return __shfl_sync(kFull, v, 0); }
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float middle_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -175,16 +179,19 @@ __device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void* src)
 // warp makes at once fall into different banks.
 template <int NG>
 struct Stage {
-    static constexpr int K = 0, V = 1024, KP = 2048, VP = KP + 64 * NG, MASK = VP + 64 * NG, bytes = MASK + 16;
+    static constexpr int K = 0, V = 1024, KP = 2048, VP = KP + 64 * NG, MASK = VP + 64 * NG, bytes = MASK + 32;
 };
+// a warp's shared memory: its ring, and a tile's unpacked parameters (floats
+// [K scale, K middle, V scale * c_G, V middle][16 rows][NG])
 template <int NG>
-constexpr int kSmem = kWarps * kStages * Stage<NG>::bytes;
+constexpr int kWarpSmem = kStages * Stage<NG>::bytes + 256 * NG;
 
 // NG: groups of a row.  NT: blocks of 4 query heads.  A lane is (g, t) =
 // (lane / 4, lane % 4).
 template <int NG, int NT>
 struct Warp {
     static constexpr int NGH = NG > 1 ? NG / 2 : 1;    // groups whose middles this lane's half (g / 4) sums
+    static constexpr int W = NG == 4 ? 2 : 1;          // parameter words of a cache that this lane unpacks per tile
 
     uint32_t qa[NT][4][4];   // digits of q: A of the k32 step j
     float qs[NT][NGH];       // sum of q over a group, in units of the lane's integer logit
@@ -192,8 +199,9 @@ struct Warp {
     float m[NT], l[NT];      // running maximum and this lane's share of the sum, head 4 nt + g % 4
     float Z[NT][NGH];        // this lane's share of sum p * middle
     float acc[NT][8][4];     // sum (p s c_G) code: [channel block J, pair of channels][..]
-    float c[NG];
-    uint32_t top[2];         // largest scale bits that c allows, of the groups this lane watches
+    uint32_t magic, offset;  // of codes_low and codes_high
+    int base[4];             // what integer sums start at
+    float c[W];              // the powers of two c_G of the groups whose parameters this lane unpacks
 
     // ---- the unit's queries
     __device__ __forceinline__ void start(const Kv4AttendArgs& a, const Unit& x, bool bf16)
@@ -234,18 +242,20 @@ struct Warp {
             }
             const bool bad = nan != 0.f;                       // an infinity or a NaN in the head
             if (bad) top_q = 0.f;
-            // |q| < 2^e; q = X 2^(e - 27)
-            const int e = top_q > 0.f ? (int)((__double_as_longlong((double)top_q) >> 52) & 2047) - 1022 : 0;
-            const double to_fixed = __longlong_as_double((long long)(1023 + 27 - e) << 52);
-            const double unit = __longlong_as_double((long long)(1023 + e - 27) << 52);
-            long long sum[4];
+            // |q| < 2^e; q = X 2^(e - 27), the power of two in two factors (each a float)
+            const bool small = top_q < 1.5777218e-30f;         // 2^-99
+            int e = (int)(__float_as_uint(small ? top_q * 1.8446744e19f : top_q) >> 23) - 126 - (small ? 64 : 0);
+            if (top_q == 0.f) e = 0;
+            const int half = (27 - e) / 2;
+            const float up1 = __uint_as_float((uint32_t)(127 + half) << 23), up2 = __uint_as_float((uint32_t)(127 + 27 - e - half) << 23);
+            float sum[4];                                      // over 32 channels, in units of 4 X
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t d[4] = {0u, 0u, 0u, 0u};              // [channels 4..7 / 0..3 of 8 t ..][first / second digit]
                 int part = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int X = bad ? 0 : __double2int_rn((double)q[j][i] * to_fixed);
+                    const int X = bad ? 0 : __float2int_rn(q[j][i] * up1 * up2);
                     part += X;                                 // 8 * 2^27 at most
                     const int d3 = ((X + 64) & 127) - 64, X1 = (X - d3) >> 7;
                     const int d2 = ((X1 + 64) & 127) - 64, X2 = (X1 - d2) >> 7;
@@ -257,21 +267,22 @@ struct Warp {
                 // rows g and g + 8 of A: the lane half's first and second digit
 #pragma unroll
                 for (int i = 0; i < 4; ++i) qa[nt][j][i] = d[i];
-                sum[j] = part;
-                sum[j] += __shfl_xor_sync(kFull, sum[j], 1);
-                sum[j] += __shfl_xor_sync(kFull, sum[j], 2);
+                part >>= 2;                                    // so that four of them fit; 2^-25 of the largest channel
+                part += __shfl_xor_sync(kFull, part, 1);
+                part += __shfl_xor_sync(kFull, part, 2);
+                sum[j] = (float)part;
             }
             // a lane's integer logit counts units of 2^14 (first half) or 1, times 16 (the codes)
-            const double in_units = (g < 4 ? 1.0 / 16384.0 : 1.0) * 16.0;
+            const float in_units = (g < 4 ? 1.f / 16384.f : 1.f) * 16.f * 4.f;
             if constexpr (NG == 4) {
-                qs[nt][0] = (float)((double)(g < 4 ? sum[0] : sum[2]) * in_units);
-                qs[nt][1] = (float)((double)(g < 4 ? sum[1] : sum[3]) * in_units);
+                qs[nt][0] = (g < 4 ? sum[0] : sum[2]) * in_units;
+                qs[nt][1] = (g < 4 ? sum[1] : sum[3]) * in_units;
             } else if constexpr (NG == 2) {
-                qs[nt][0] = (float)((double)(g < 4 ? sum[0] + sum[1] : sum[2] + sum[3]) * in_units);
+                qs[nt][0] = (g < 4 ? sum[0] + sum[1] : sum[2] + sum[3]) * in_units;
             } else {
-                qs[nt][0] = (float)((double)(sum[0] + sum[1] + sum[2] + sum[3]) * 0.5 * in_units);
+                qs[nt][0] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * (0.5f * in_units);
             }
-            F[nt] = bad ? NAN : (float)(unit * kLog2Scale * (g < 4 ? 1024.0 : 0.0625));
+            F[nt] = bad ? NAN : 1.f / up1 / up2 * (kLog2Scale * (g < 4 ? 1024.f : 0.0625f));
             m[nt] = -FLT_MAX;
             l[nt] = 0.f;
 #pragma unroll
@@ -281,46 +292,43 @@ struct Warp {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[nt][i][r] = 0.f;
         }
+        magic = held(0x64886488u);
+        offset = held(0xd488d488u);
 #pragma unroll
-        for (int j = 0; j < NG; ++j) c[j] = 1.2676506e30f;     // 2^100: scales below 2^-86
-        top[0] = top[1] = ((uint32_t)(127 - 86) << 23) - 1u;
+        for (int i = 0; i < 4; ++i) base[i] = (int)held(0x4b400000u);
+#pragma unroll
+        for (int j = 0; j < W; ++j) c[j] = 1.2676506e30f;      // 2^100: scales below 2^-86
     }
 
-    // ---- larger value scales than so far: c_G down, sums with it
-    __device__ __forceinline__ void raise(uint32_t w0, uint32_t w1)
+    // the lane and word that hold group j's c
+    static __device__ __forceinline__ int c_lane(int j) { return NG == 4 ? j >> 1 : NG == 2 ? j : 0; }
+
+    // ---- larger value scales than so far (this lane's are sc): c_G down, sums with it
+    __device__ __forceinline__ void raise(const float (&sc)[W])
     {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            uint32_t v = 0u;
-            if (NG == 4) v = (lane & 1) == (j >> 1) ? (j & 1 ? w1 : w0) << 16 : 0u;
-            else if (NG == 2) v = (lane & 1) == j ? w0 << 16 : 0u;
-            else v = w0 << 16;
-            const uint32_t most = __reduce_max_sync(kFull, v);
+            const bool mine = NG == 1 || (lane & 1) == c_lane(j);
+            const uint32_t most = __reduce_max_sync(kFull, mine ? __float_as_uint(sc[j % W]) : 0u);
             // scale < 2^e
             int e = (int)((most >> 23) & 255u) - 126;
             e = e < -86 ? -86 : e;
-            const float now = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            if (now < c[j]) {
-                const float f = now / c[j];
+            const float was = __shfl_sync(kFull, c[j % W], c_lane(j)), now = fminf(was, __uint_as_float((uint32_t)(127 + 14 - e) << 23));
+            const float f = now / was;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int J = 0; J < 4; ++J)
-                        if (J * NG / 4 == j)
+                for (int J = 0; J < 4; ++J)
+                    if (J * NG / 4 == j)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) { acc[nt][2 * J][r] *= f; acc[nt][2 * J + 1][r] *= f; }
-                c[j] = now;
-                const uint32_t limit = ((uint32_t)(e + 127) << 23) - 1u;
-                if (NG == 4) { if ((lane & 1) == (j >> 1)) top[j & 1] = limit; }
-                else if (NG == 2) { if ((lane & 1) == j) top[0] = limit; }
-                else top[0] = limit;
-            }
+                        for (int r = 0; r < 4; ++r) { acc[nt][2 * J][r] *= f; acc[nt][2 * J + 1][r] *= f; }
+            if (mine) c[j % W] = now;
         }
     }
 
     // ---- one tile; valid: its rows (bit = row of the tile)
-    __device__ __forceinline__ void tile(unsigned char* st, uint32_t valid)
+    __device__ __forceinline__ void tile(const unsigned char* st, unsigned char* un, uint32_t valid)
     {
         using S = Stage<NG>;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -328,12 +336,30 @@ struct Warp {
         // MMAs; their order within the pair alternates with t (see Stage)
         const int ra = 2 * t + (t & 1), rb = 2 * t + 1 - (t & 1);
         const int rows[4] = {ra, rb, ra + 8, rb + 8};
-        if (valid != 0xffffu) {
-            // rows that are not there: their parameters may be anything
-            if (!((valid >> (lane & 15)) & 1u)) {
-                uint32_t* p = reinterpret_cast<uint32_t*>(st + (lane < 16 ? S::KP : S::VP)) + (lane & 15) * NG;
+        // ---- parameters: each word is unpacked by one lane, not by the eight that use it
+        {
+            const int word = NG == 4 ? 2 * lane : NG == 2 ? lane : lane & 15;
+            Words<W> kw = lds<W>(st + S::KP + 4 * word), vw = lds<W>(st + S::VP + 4 * word);
+            if (valid != 0xffffu && !((valid >> (NG == 1 ? lane & 15 : lane >> 1)) & 1u)) {
+                // a row that is not there: its parameters may be anything
 #pragma unroll
-                for (int j = 0; j < NG; ++j) p[j] = 0u;
+                for (int i = 0; i < W; ++i) kw.w[i] = vw.w[i] = 0u;
+            }
+            float sc[W];
+            bool more = false;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                sc[i] = scale_of(vw.w[i]);
+                more |= sc[i] * c[i] >= 16384.f;
+            }
+            if (__any_sync(kFull, more)) raise(sc);
+            float* u = reinterpret_cast<float*>(un) + word;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                u[i] = scale_of(kw.w[i]);
+                u[16 * NG + i] = middle_of(kw.w[i]);
+                u[32 * NG + i] = sc[i] * c[i];
+                u[48 * NG + i] = middle_of(vw.w[i]);
             }
             __syncwarp();
         }
@@ -343,12 +369,12 @@ struct Warp {
             float ks[4][NG], km[4][NGH];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const Words<NG> w = lds<NG>(st + S::KP + rows[e] * (4 * NG));
+                const Words<NG> w = lds<NG>(un + rows[e] * (4 * NG));
+                const Words<NGH> h = lds<NGH>(un + 64 * NG + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
 #pragma unroll
-                for (int j = 0; j < NG; ++j) ks[e][j] = scale_of(w.w[j]);
-                const Words<NGH> h = lds<NGH>(st + S::KP + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
+                for (int j = 0; j < NG; ++j) ks[e][j] = __uint_as_float(w.w[j]);
 #pragma unroll
-                for (int j = 0; j < NGH; ++j) km[e][j] = middle_of(h.w[j]);
+                for (int j = 0; j < NGH; ++j) km[e][j] = __uint_as_float(h.w[j]);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -360,6 +386,11 @@ struct Warp {
                 }
             // column n of MMA a is row 8 a + rowof(n): lane g loads that row
             const int kr = 2 * (g >> 1) + ((g & 1) ^ ((g >> 1) & 1));
+            // The sums start at the bits of 1.5 * 2^23, so that they are floats
+            // 1.5 * 2^23 + v for |v| < 2^22: no conversion.  128 v0 + v1, the two
+            // digits' sums, is then one FMA that also takes the offsets off
+            // (exact) and one add that rounds.
+            constexpr float kOff = -129.f * 12582912.f;
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 const Words<4> w = lds<4>(st + S::K + (8 * a + kr) * kRowCodes + 16 * t);
@@ -367,17 +398,17 @@ struct Warp {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t b0 = w.w[j] & 0xf0f0f0f0u, b1 = (w.w[j] << 4) & 0xf0f0f0f0u;
-                    const int zero[4] = {0, 0, 0, 0};
                     constexpr int per = 4 / NG;                // k32 steps of a group
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        if (j % per == 0) mma_s8(d[nt], qa[nt][j], b0, b1, zero);
+                        if (j % per == 0) mma_s8(d[nt], qa[nt][j], b0, b1, base);
                         else mma_s8(d[nt], qa[nt][j], b0, b1, d[nt]);
                         if (j % per == per - 1) {
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                z[nt][2 * a + i] = fmaf(ks[2 * a + i][j / per], (float)(d[nt][i] * 128 + d[nt][2 + i]),
-                                                        z[nt][2 * a + i]);
+                            for (int i = 0; i < 2; ++i) {
+                                const float v = fmaf(__int_as_float(d[nt][i]), 128.f, kOff) + __int_as_float(d[nt][2 + i]);
+                                z[nt][2 * a + i] = fmaf(ks[2 * a + i][j / per], v, z[nt][2 * a + i]);
+                            }
                         }
                     }
                 }
@@ -421,12 +452,6 @@ struct Warp {
                 }
             }
         }
-        // ---- larger scales among the values (each lane looks at two words of the parameters)
-        {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(st + S::VP);
-            const uint32_t w0 = NG == 4 ? p[2 * lane] : NG == 2 ? p[lane] : p[lane & 15], w1 = NG == 4 ? p[2 * lane + 1] : 0u;
-            if (__any_sync(kFull, (w0 << 16) > top[0] || (NG == 4 && (w1 << 16) > top[1]))) raise(w0, w1);
-        }
         // ---- weights, and their products with the scales
         uint32_t pb[NT][NG][2];
         {
@@ -441,14 +466,14 @@ struct Warp {
             float vs[4][NG];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const Words<NG> w = lds<NG>(st + S::VP + rows[e] * (4 * NG));
+                const Words<NG> w = lds<NG>(un + 128 * NG + rows[e] * (4 * NG));
+                const Words<NGH> h = lds<NGH>(un + 192 * NG + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
 #pragma unroll
-                for (int j = 0; j < NG; ++j) vs[e][j] = scale_of(w.w[j]) * c[j];
-                const Words<NGH> h = lds<NGH>(st + S::VP + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
+                for (int j = 0; j < NG; ++j) vs[e][j] = __uint_as_float(w.w[j]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < NGH; ++j) Z[nt][j] = fmaf(p[nt][e], middle_of(h.w[j]), Z[nt][j]);
+                    for (int j = 0; j < NGH; ++j) Z[nt][j] = fmaf(p[nt][e], __uint_as_float(h.w[j]), Z[nt][j]);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -474,7 +499,8 @@ struct Warp {
             uint32_t x = __byte_perm(v[0].w[J >> 1], v[1].w[J >> 1], sel), y = __byte_perm(v[2].w[J >> 1], v[3].w[J >> 1], sel);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t a0 = codes_low(x), a1 = codes_high(x), a2 = codes_low(y), a3 = codes_high(y);
+                const uint32_t a0 = codes_low(x, magic), a1 = codes_high(x, magic, offset);
+                const uint32_t a2 = codes_low(y, magic), a3 = codes_high(y, magic, offset);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     mma_f16(acc[nt][2 * J + k], a0, a1, a2, a3, pb[nt][J * NG / 4][0], pb[nt][J * NG / 4][1]);
@@ -492,7 +518,7 @@ struct Warp {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int J = 0; J < 4; ++J) {
-                const float inv = 1.f / c[J * NG / 4];
+                const float inv = 1.f / __shfl_sync(kFull, c[J * NG / 4 % W], c_lane(J * NG / 4));
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -521,6 +547,96 @@ struct Warp {
 // weight of a part with maximum m and sum l in a merge with maximum M; a part without rows has l = 0
 __device__ __forceinline__ float part_weight(float m, float l, float M) { return l == 0.f ? 0.f : ex2(m - M); }
 
+// channel d of head h over the CTA's warps, and their maximum and sum
+template <int NG>
+__device__ __forceinline__ float merge_warps(const float* red, int stride, int h, int d, float& M, float& L)
+{
+    const float* r = red + h * kRed;
+    float O = 0.f;
+    M = -FLT_MAX;
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, r[w * stride + kD]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float* rw = r + w * stride;
+        const float f = part_weight(rw[kD], rw[kD + 1], M);
+        L += f * rw[kD + 1];
+        O += f * (rw[d] + rw[kD + 2 + d * NG / kD]);
+    }
+    return O;
+}
+
+__device__ __forceinline__ void store_out(const Kv4AttendArgs& a, const Unit& x, int h, int d, float O, float M, float L)
+{
+    const int64_t hq = (int64_t)x.b * a.Hq + x.head0 + h;
+    a.out[hq * kD + d] = L == 0.f ? 0.f : O / L;
+    if (d == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// The CTA merges slots u + pf .. u + pf + ns - 1 of unit u.  First a warp per
+// head turns the slots' (m, l) into weights, a lane a slot; then a thread
+// takes 4 channels of a head and every k-th slot, with independent loads.
+__device__ __forceinline__ void merge_slots(const Kv4AttendArgs& a, const Unit& x, int u, int pf, int ns, float* sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float* weight = sh;                                    // [NH][ns]
+    float* total = weight + a.NH * ns;                     // [NH][2]: m, l
+    float4* part = reinterpret_cast<float4*>(sh + kKv4MaxHeads * (kKv4MaxCtas + 2));   // [kThreads]
+    const float2* sm = reinterpret_cast<const float2*>(a.part + (int64_t)(a.U + kKv4MaxCtas) * a.NH * kD) + (int64_t)(u + pf) * a.NH;
+    const float4* so = reinterpret_cast<const float4*>(a.part + (int64_t)(u + pf) * a.NH * kD);
+    for (int h = warp; h < a.NH; h += kWarps) {
+        float M = -FLT_MAX, L = 0.f;
+        for (int s = lane; s < ns; s += 32) M = fmaxf(M, __ldcg(sm + (int64_t)s * a.NH + h).x);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
+        for (int s = lane; s < ns; s += 32) {
+            const float2 v = __ldcg(sm + (int64_t)s * a.NH + h);
+            const float f = part_weight(v.x, v.y, M);
+            weight[h * ns + s] = f;
+            L += f * v.y;
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(kFull, L, off);
+        if (lane == 0) { total[2 * h] = M; total[2 * h + 1] = L; }
+    }
+    __syncthreads();
+    constexpr int kQuads = kD / 4;
+    const int items = a.NH * kQuads, ways = kThreads / items;   // NH <= 8: one item a thread at most
+    const int item = tid % items, way = tid / items;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (way < ways) {
+        const float* w = weight + item / kQuads * ns;
+#pragma unroll 4
+        for (int s = way; s < ns; s += ways) {
+            const float4 v = __ldcg(so + (int64_t)s * items + item);
+            const float f = w[s];
+            o.x += f * v.x;
+            o.y += f * v.y;
+            o.z += f * v.z;
+            o.w += f * v.w;
+        }
+        part[tid] = o;
+    }
+    __syncthreads();
+    if (tid < items) {
+        for (int i = 1; i < ways; ++i) {
+            const float4 v = part[i * items + tid];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+        }
+        const int h = tid / kQuads;
+        const int64_t hq = (int64_t)x.b * a.Hq + x.head0 + h;
+        const float L = total[2 * h + 1];
+        if (L == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        else { o.x /= L; o.y /= L; o.z /= L; o.w /= L; }
+        reinterpret_cast<float4*>(a.out)[hq * kQuads + tid % kQuads] = o;
+        if (a.lse && tid % kQuads == 0) a.lse[hq] = L == 0.f ? -INFINITY : (total[2 * h] + log2f(L)) * 0.6931471805599453f;
+    }
+}
+
 // CTAs of an SM: two while a warp's sums fit 128 registers
 template <int NT>
 constexpr int kCtasPerSM = NT == 1 ? 2 : 1;
@@ -529,15 +645,17 @@ template <int NG, int NT, bool ROWS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const __grid_constant__ Kv4AttendArgs a, int bf16)
 {
     using S = Stage<NG>;
-    static_assert(4 * NT * kRed * 4 <= kStages * S::bytes, "a warp's results must fit its ring");
+    static_assert(4 * NT * kRed * 4 <= kWarpSmem<NG>, "a warp's results must fit its ring");
+    static_assert(kWarpSmem<NG> % 128 == 0, "aligned warps");
+    static_assert(kKv4MaxHeads * (kKv4MaxCtas + 2) * 4 + kThreads * 16 <= kWarps * kWarpSmem<NG>, "the merge must fit");
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long s_scan[kWarps];
     __shared__ long long s_first[2];       // first unit of this CTA's share, tiles before that unit
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned char* ring = smem + warp * (kStages * S::bytes);
+    unsigned char* ring = smem + warp * kWarpSmem<NG>;
     float* red = reinterpret_cast<float*>(smem);
-    constexpr int kRedWarp = kStages * S::bytes / 4;       // floats between two warps' results
+    constexpr int kRedWarp = kWarpSmem<NG> / 4;            // floats between two warps' results
     const int p = blockIdx.x;
 
     // ---- the share: tiles of all units, and the unit the share starts in
@@ -609,36 +727,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
             const int first = t0 + warp;
             const int nb = t1 > first ? (t1 - first + kWarps - 1) / kWarps : 0;
             const int64_t row0 = ((int64_t)x.b * a.Hkv + x.kvh) * a.K4.R;
-            const unsigned char* kc = a.K4.codes + row0 * kRowCodes;
-            const unsigned char* vc = a.V4.codes + row0 * kRowCodes;
-            const uint32_t* par = (lane < 16 ? a.K4.params : a.V4.params) + row0 * NG;
-            const uint32_t ring_at = smem_u32(ring);
             const int r8 = lane >> 2, ch = lane & 3;
+            // this lane's bytes of the first tile (dense) or of row 0 (rows)
+            const int64_t from = row0 + (ROWS ? 0 : (int64_t)first * kTile);
+            const unsigned char* kc = a.K4.codes + (from + (ROWS ? 0 : r8)) * kRowCodes + 16 * ch;
+            const unsigned char* vc = a.V4.codes + (from + (ROWS ? 0 : r8)) * kRowCodes + 16 * ch;
+            const uint32_t* par = (lane < 16 ? a.K4.params : a.V4.params) + (from + (ROWS ? 0 : lane & 15)) * NG;
+            const uint32_t ring_at = smem_u32(ring);
+            const uint32_t to_k = r8 * kRowCodes + 16 * ch, to_v = S::V + r8 * kRowCodes + 16 * (ch ^ ((r8 >> 1) & 2));
+            const uint32_t to_p = S::KP + lane * (4 * NG);
             // entry (lane % 16) of the warp's tile i: its position, -1 for none
             auto entry = [&](int i) { return i < nb ? entry_row(a, x, u, (first + i * kWarps) * kTile + (lane & 15)) : -1; };
             auto issue = [&](int i, int row) {
                 if (i < nb) {
                     const uint32_t st = ring_at + (i % kStages) * S::bytes;
-                    int k0, k1, pr;
                     if (ROWS) {
                         const uint32_t mask = __ballot_sync(kFull, row >= 0) & 0xffffu;
                         row = max(row, 0);
-                        k0 = __shfl_sync(kFull, row, r8);
-                        k1 = __shfl_sync(kFull, row, r8 + 8);
-                        pr = row;
+                        const int64_t k0 = (int64_t)__shfl_sync(kFull, row, r8) * kRowCodes;
+                        const int64_t k1 = (int64_t)__shfl_sync(kFull, row, r8 + 8) * kRowCodes;
                         if (lane == 0) *reinterpret_cast<uint32_t*>(ring + (i % kStages) * S::bytes + S::MASK) = mask;
+                        cp_async_bytes<16>(st + to_k, kc + k0);
+                        cp_async_bytes<16>(st + to_k + 8 * kRowCodes, kc + k1);
+                        cp_async_bytes<16>(st + to_v, vc + k0);
+                        cp_async_bytes<16>(st + to_v + 8 * kRowCodes, vc + k1);
+                        cp_async_bytes<4 * NG>(st + to_p, par + (int64_t)row * NG);
                     } else {
-                        const int base = (first + i * kWarps) * kTile;   // the cache's rows are padded to whole tiles
-                        k0 = base + r8;
-                        k1 = k0 + 8;
-                        pr = base + (lane & 15);
+                        // the cache's rows are padded to whole tiles
+                        cp_async_bytes<16>(st + to_k, kc);
+                        cp_async_bytes<16>(st + to_k + 8 * kRowCodes, kc + 8 * kRowCodes);
+                        cp_async_bytes<16>(st + to_v, vc);
+                        cp_async_bytes<16>(st + to_v + 8 * kRowCodes, vc + 8 * kRowCodes);
+                        cp_async_bytes<4 * NG>(st + to_p, par);
+                        kc += kWarps * kTile * kRowCodes;
+                        vc += kWarps * kTile * kRowCodes;
+                        par += kWarps * kTile * NG;
                     }
-                    const int sw = (r8 >> 1) & 2;
-                    cp_async_bytes<16>(st + S::K + r8 * kRowCodes + 16 * ch, kc + (int64_t)k0 * kRowCodes + 16 * ch);
-                    cp_async_bytes<16>(st + S::K + (r8 + 8) * kRowCodes + 16 * ch, kc + (int64_t)k1 * kRowCodes + 16 * ch);
-                    cp_async_bytes<16>(st + S::V + r8 * kRowCodes + 16 * (ch ^ sw), vc + (int64_t)k0 * kRowCodes + 16 * ch);
-                    cp_async_bytes<16>(st + S::V + (r8 + 8) * kRowCodes + 16 * (ch ^ sw), vc + (int64_t)k1 * kRowCodes + 16 * ch);
-                    cp_async_bytes<4 * NG>(st + S::KP + lane * (4 * NG), par + (int64_t)pr * NG);
                 }
                 cp_async_commit();
             };
@@ -658,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
                 issue(i + kStages - 1, now);
                 cp_async_wait<kStages - 1>();
                 __syncwarp();
-                unsigned char* st = ring + (i % kStages) * S::bytes;
+                const unsigned char* st = ring + (i % kStages) * S::bytes;
                 uint32_t valid = 0xffffu;
                 if (ROWS) {
                     valid = *reinterpret_cast<const uint32_t*>(st + S::MASK);
@@ -666,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
                     const int left = x.count - (first + i * kWarps) * kTile;
                     if (left < kTile) valid = (1u << left) - 1u;
                 }
-                w.tile(st, valid);
+                w.tile(st, ring + kStages * S::bytes, valid);
                 __syncwarp();
             }
             cp_async_wait<0>();
@@ -674,49 +798,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
             w.finish(reinterpret_cast<float*>(ring));          // the ring is drained
         }
         __syncthreads();
-        // ---- the piece's slot: the warps merged per head
-        float* slot = a.part + (int64_t)(u + p) * a.NH * kSlot;
-        for (int i = tid; i < a.NH * kD; i += kThreads) {
-            const int h = i / kD, d = i % kD;
-            const float* r = red + h * kRed;
-            float M = -FLT_MAX, L = 0.f, O = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, r[w * kRedWarp + kD]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float* rw = r + w * kRedWarp;
-                const float f = part_weight(rw[kD], rw[kD + 1], M);
-                L += f * rw[kD + 1];
-                O += f * (rw[d] + rw[kD + 2 + d * NG / kD]);
-            }
-            slot[h * kSlot + 2 + d] = O;
-            if (d == 0) { slot[h * kSlot] = M; slot[h * kSlot + 1] = L; }
-        }
-        __threadfence();
-        __syncthreads();
-        // ---- arrival; the unit's last piece merges every slot
         const int pf = owner_of(before, TT, P), pl = owner_of(end - 1, TT, P);
-        if (tid == 0) s_last = atomicAdd(a.cnt + u, 1u) == (unsigned)(pl - pf);
-        __syncthreads();
-        if (s_last) {
-            __threadfence();
-            const float* s0 = a.part + (int64_t)(u + pf) * a.NH * kSlot;
+        if (pf == pl) {
+            // the unit is this piece
             for (int i = tid; i < a.NH * kD; i += kThreads) {
-                const int h = i / kD, d = i % kD;
-                float M = -FLT_MAX, L = 0.f, O = 0.f;
-                for (int s = 0; s <= pl - pf; ++s) M = fmaxf(M, __ldcg(s0 + ((int64_t)s * a.NH + h) * kSlot));
-                for (int s = 0; s <= pl - pf; ++s) {
-                    const float* q = s0 + ((int64_t)s * a.NH + h) * kSlot;
-                    const float ls = __ldcg(q + 1);
-                    const float f = part_weight(__ldcg(q), ls, M);
-                    L += f * ls;
-                    O += f * __ldcg(q + 2 + d);
-                }
-                const int64_t hq = (int64_t)x.b * a.Hq + x.head0 + h;
-                a.out[hq * kD + d] = L == 0.f ? 0.f : O / L;
-                if (d == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+                float M, L;
+                const float O = merge_warps<NG>(red, kRedWarp, i / kD, i % kD, M, L);
+                store_out(a, x, i / kD, i % kD, O, M, L);
             }
-            if (tid == 0) a.cnt[u] = 0;
+        } else {
+            // ---- the piece's slot
+            float* so = a.part + (int64_t)(u + p) * a.NH * kD;
+            float2* sm = reinterpret_cast<float2*>(a.part + (int64_t)(a.U + kKv4MaxCtas) * a.NH * kD) + (int64_t)(u + p) * a.NH;
+            for (int i = tid; i < a.NH * kD; i += kThreads) {
+                float M, L;
+                so[i] = merge_warps<NG>(red, kRedWarp, i / kD, i % kD, M, L);
+                if (i % kD == 0) sm[i / kD] = make_float2(M, L);
+            }
+            __threadfence();
+            __syncthreads();
+            // ---- arrival; the unit's last piece merges every slot
+            if (tid == 0) s_last = atomicAdd(a.cnt + u, 1u) == (unsigned)(pl - pf);
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                merge_slots(a, x, u, pf, pl - pf + 1, red);
+                if (tid == 0) a.cnt[u] = 0;
+            }
         }
         __syncthreads();   // the rings are written again by the next piece
         at = before + t1;
@@ -728,14 +836,14 @@ template <int NG, int NT, bool ROWS>
 cudaError_t launch_attend_t(const Kv4AttendArgs& a, int bf16, int sms, cudaStream_t st)
 {
     auto fn = k_kv4_attend<NG, NT, ROWS>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<NG>);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kWarpSmem<NG>);
     if (e != cudaSuccess) return e;
     long long tiles = ROWS ? ((long long)a.S + a.max_rows + 1 + kTile - 1) / kTile : (a.n + kTile - 1) / kTile;
     tiles *= a.U;
     long long P = (tiles + kWarps - 1) / kWarps;
     P = P < (long long)kCtasPerSM<NT> * sms ? P : (long long)kCtasPerSM<NT> * sms;
     P = P < kKv4MaxCtas ? P : kKv4MaxCtas;
-    fn<<<(unsigned)P, kThreads, kSmem<NG>, st>>>(a, bf16);
+    fn<<<(unsigned)P, kThreads, kWarps * kWarpSmem<NG>, st>>>(a, bf16);
     return cudaGetLastError();
 }
 

@@ -198,7 +198,7 @@ struct Kv4AttendArgs {
     const int32_t* rows;             // [U][max_rows], or null: dense
     const int32_t* n_rows;           // [U]
     int max_rows, S;
-    float* part;                     // [U + kKv4MaxCtas][NH][2 + D]
+    float* part;                     // o [U + kKv4MaxCtas][NH][D], then (m, l) [U + kKv4MaxCtas][NH][2]
     unsigned* cnt;                   // [U] arrivals, 0 between calls
     float* out;                      // [B][Hq][D]
     float* lse;                      // [B][Hq] or null
