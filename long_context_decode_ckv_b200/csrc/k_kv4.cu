@@ -15,11 +15,15 @@
 //     4 digits), a nibble in the high half of a byte as the code times 16;
 //     unpacking 8 codes takes 3 instructions and no conversion.
 //   (p s).c on the fp16 MMA: codes as fp16 integers, p s as two fp16 parts
-//     (22 bits) in the 8 columns of B (4 heads x 2 parts), times a power of
-//     two c_G that keeps the largest below 2^14.
+//     (22 bits) in the 8 columns of B (4 heads x 2 parts).  p, 2^9 for the largest weight, is
+//     split once into p1 + p2, and a scale, times a power of two c_G that keeps
+//     the largest below 2, has 8 bits: h = fp16(p1 s), and the second part
+//     p1 s - h + p2 s is two fused fp16 operations, the first one exact.
+//     What a weight loses is below 2^-34 of the largest one, and a scale keeps
+//     its 8 bits down to 2^-18 of the largest of its group.
 //
 // Work split: one unit per (batch, KV head), or per row list.  Units' tiles of
-// 16 rows are laid end to end and split evenly over the grid; a CTA's share
+// 32 rows are laid end to end and split evenly over the grid; a CTA's share
 // is one or more pieces (a run of one unit's tiles), and its warps take the
 // tiles of a piece in turn, each through its own ring of cp.async stages.  A
 // piece's (m, l, o) per head goes to a slot of its own; the unit's last piece
@@ -40,8 +44,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;                 // rows of a tile
-constexpr int kStages = 4;                // tiles of a warp's ring
+constexpr int kTile = 32;                 // rows of a tile: two MMA tiles of 16
+constexpr int kStages = 2;                // tiles of a warp's ring
 constexpr int kRed = kD + 2 + 4;          // a warp's result per head: o[D], m, l, the middles' sums
 constexpr float kLog2Scale = (float)(0.08838834764831845 * 1.4426950408889634);   // log2(e) / sqrt(128)
 
@@ -144,6 +148,18 @@ __device__ __forceinline__ uint32_t codes_high(uint32_t x, uint32_t magic, uint3
 // and the compiler, which cannot see through the shuffle, would otherwise
 // rebuild the other one at every use
 __device__ __forceinline__ uint32_t held(uint32_t v) { return __shfl_sync(kFull, v, 0); }
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float middle_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -167,41 +183,57 @@ __device__ __forceinline__ Words<N> lds(const unsigned char* p)
     return r;
 }
 template <int N>
+__device__ __forceinline__ void sts(unsigned char* p, const Words<N>& r)
+{
+    if constexpr (N == 4) *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else if constexpr (N == 2) *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = r.w[0];
+}
+template <int N>
 __device__ __forceinline__ void cp_async_bytes(uint32_t dst, const void* src)
 {
     if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 
-// One stage of a warp's ring: 16 rows of K codes, V codes, K parameters, V
-// parameters and the rows' mask.  V's 16-byte chunks of rows 4-7 and 12-15
-// are swapped by halves, so that the 8-byte reads of four rows that a half
+// One stage of a warp's ring: a tile's K codes, V codes, K parameters, V
+// parameters and the rows' mask.  V's 16-byte chunks of rows 4-7 and 12-15 of
+// 16 are swapped by halves, so that the 8-byte reads of four rows that a half
 // warp makes at once fall into different banks.
 template <int NG>
 struct Stage {
-    static constexpr int K = 0, V = 1024, KP = 2048, VP = KP + 64 * NG, MASK = VP + 64 * NG, bytes = MASK + 32;
+    static constexpr int K = 0, V = K + kTile * kRowCodes, KP = V + kTile * kRowCodes, VP = KP + kTile * 4 * NG,
+                         MASK = VP + kTile * 4 * NG, bytes = MASK + 32;
 };
-// a warp's shared memory: its ring, and a tile's unpacked parameters (floats
-// [K scale, K middle, V scale * c_G, V middle][16 rows][NG])
+// a tile's unpacked parameters: K scales, K middles, V middles as floats
+// [32 rows][NG], V scales times c_G as fp16 pairs [16 pairs of rows][NG]
 template <int NG>
-constexpr int kWarpSmem = kStages * Stage<NG>::bytes + 256 * NG;
+struct Unpacked {
+    static constexpr int KS = 0, KM = kTile * 4 * NG, VM = 2 * KM, VS = 3 * KM, bytes = VS + kTile * 2 * NG;
+};
+// a warp's shared memory: its ring, and a tile's unpacked parameters
+template <int NG>
+constexpr int kWarpSmem = (kStages * Stage<NG>::bytes + Unpacked<NG>::bytes + 127) / 128 * 128;
+// Weights are powers of two of z - max + kRef: 2^kRef for the largest logit
+// when the reference was set, at most 2^kMost before it is set again (a new
+// maximum moves it only then; each move costs a pass over the sums).
+constexpr float kRef = 9.f, kMost = 14.f;
 
 // NG: groups of a row.  NT: blocks of 4 query heads.  A lane is (g, t) =
 // (lane / 4, lane % 4).
 template <int NG, int NT>
 struct Warp {
     static constexpr int NGH = NG > 1 ? NG / 2 : 1;    // groups whose middles this lane's half (g / 4) sums
-    static constexpr int W = NG == 4 ? 2 : 1;          // parameter words of a cache that this lane unpacks per tile
 
     uint32_t qa[NT][4][4];   // digits of q: A of the k32 step j
     float qs[NT][NGH];       // sum of q over a group, in units of the lane's integer logit
     float F[NT];             // logit (in powers of two) of one such unit
-    float m[NT], l[NT];      // running maximum and this lane's share of the sum, head 4 nt + g % 4
+    float m[NT], l[NT];      // kRef - the maximum referred to, and this lane's share of the sum: head 4 nt + g % 4
     float Z[NT][NGH];        // this lane's share of sum p * middle
     float acc[NT][8][4];     // sum (p s c_G) code: [channel block J, pair of channels][..]
     uint32_t magic, offset;  // of codes_low and codes_high
     int base[4];             // what integer sums start at
-    float c[W];              // the powers of two c_G of the groups whose parameters this lane unpacks
+    float c[NG];             // the powers of two c_G
 
     // ---- the unit's queries
     __device__ __forceinline__ void start(const Kv4AttendArgs& a, const Unit& x, bool bf16)
@@ -283,7 +315,7 @@ struct Warp {
                 qs[nt][0] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * (0.5f * in_units);
             }
             F[nt] = bad ? NAN : 1.f / up1 / up2 * (kLog2Scale * (g < 4 ? 1024.f : 0.0625f));
-            m[nt] = -FLT_MAX;
+            m[nt] = FLT_MAX;
             l[nt] = 0.f;
 #pragma unroll
             for (int j = 0; j < NGH; ++j) Z[nt][j] = 0.f;
@@ -297,25 +329,20 @@ struct Warp {
 #pragma unroll
         for (int i = 0; i < 4; ++i) base[i] = (int)held(0x4b400000u);
 #pragma unroll
-        for (int j = 0; j < W; ++j) c[j] = 1.2676506e30f;      // 2^100: scales below 2^-86
+        for (int j = 0; j < NG; ++j) c[j] = 1.2676506e30f;      // 2^100: scales below 2^-99
     }
 
-    // the lane and word that hold group j's c
-    static __device__ __forceinline__ int c_lane(int j) { return NG == 4 ? j >> 1 : NG == 2 ? j : 0; }
-
-    // ---- larger value scales than so far (this lane's are sc): c_G down, sums with it
-    __device__ __forceinline__ void raise(const float (&sc)[W])
+    // ---- larger value scales than so far (this lane's row has sc): c_G down, sums with it
+    __device__ __forceinline__ void raise(const float (&sc)[NG])
     {
-        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            const bool mine = NG == 1 || (lane & 1) == c_lane(j);
-            const uint32_t most = __reduce_max_sync(kFull, mine ? __float_as_uint(sc[j % W]) : 0u);
+            const uint32_t most = __reduce_max_sync(kFull, __float_as_uint(sc[j]));
             // scale < 2^e
             int e = (int)((most >> 23) & 255u) - 126;
-            e = e < -86 ? -86 : e;
-            const float was = __shfl_sync(kFull, c[j % W], c_lane(j)), now = fminf(was, __uint_as_float((uint32_t)(127 + 14 - e) << 23));
-            const float f = now / was;
+            e = e < -99 ? -99 : e;
+            const float now = fminf(c[j], __uint_as_float((uint32_t)(127 + 1 - e) << 23)), f = now / c[j];
+            c[j] = now;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -323,54 +350,65 @@ struct Warp {
                     if (J * NG / 4 == j)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) { acc[nt][2 * J][r] *= f; acc[nt][2 * J + 1][r] *= f; }
-            if (mine) c[j % W] = now;
         }
     }
 
-    // ---- one tile; valid: its rows (bit = row of the tile)
-    __device__ __forceinline__ void tile(const unsigned char* st, unsigned char* un, uint32_t valid)
+    // ---- a tile's parameters (of stage st) into un, each row's unpacked by
+    // one lane and not by the eight that use them; valid: the tile's rows (bit
+    // = row).  Before the tile's rows16(), after the tile before.
+    __device__ __forceinline__ void unpack(const unsigned char* st, unsigned char* un, uint32_t valid)
     {
         using S = Stage<NG>;
+        using U = Unpacked<NG>;
+        const int lane = threadIdx.x & 31;
+        Words<NG> kw = lds<NG>(st + S::KP + 4 * NG * lane), vw = lds<NG>(st + S::VP + 4 * NG * lane);
+        if (!((valid >> lane) & 1u)) {
+            // a row that is not there: its parameters may be anything
+#pragma unroll
+            for (int j = 0; j < NG; ++j) kw.w[j] = vw.w[j] = 0u;
+        }
+        float sc[NG];
+        bool more = false;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            sc[j] = scale_of(vw.w[j]);
+            more |= sc[j] * c[j] >= 2.f;
+        }
+        if (__any_sync(kFull, more)) raise(sc);
+        // the pair (columns 2 t', 2 t' + 1) that the row belongs to, and which of the two it is
+        const int pair = lane >> 1, side = (lane & 1) ^ (pair & 1);
+        Words<NG> ks, km, vm;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            ks.w[j] = __float_as_uint(scale_of(kw.w[j]));
+            km.w[j] = __float_as_uint(middle_of(kw.w[j]));
+            vm.w[j] = __float_as_uint(middle_of(vw.w[j]));
+            reinterpret_cast<__half*>(un + U::VS)[2 * (pair * NG + j) + side] = __float2half_rn(sc[j] * c[j]);
+        }
+        sts<NG>(un + U::KS + 4 * NG * lane, ks);
+        sts<NG>(un + U::KM + 4 * NG * lane, km);
+        sts<NG>(un + U::VM + 4 * NG * lane, vm);
+    }
+
+    // ---- rows 16 sub .. 16 sub + 15 of a tile; valid: which are there
+    __device__ __forceinline__ void rows16(const unsigned char* st, const unsigned char* un, int sub, uint32_t valid)
+    {
+        using S = Stage<NG>;
+        using U = Unpacked<NG>;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         // the rows of this lane's logits: columns 2 t and 2 t + 1 of the two
         // MMAs; their order within the pair alternates with t (see Stage)
         const int ra = 2 * t + (t & 1), rb = 2 * t + 1 - (t & 1);
-        const int rows[4] = {ra, rb, ra + 8, rb + 8};
-        // ---- parameters: each word is unpacked by one lane, not by the eight that use it
-        {
-            const int word = NG == 4 ? 2 * lane : NG == 2 ? lane : lane & 15;
-            Words<W> kw = lds<W>(st + S::KP + 4 * word), vw = lds<W>(st + S::VP + 4 * word);
-            if (valid != 0xffffu && !((valid >> (NG == 1 ? lane & 15 : lane >> 1)) & 1u)) {
-                // a row that is not there: its parameters may be anything
-#pragma unroll
-                for (int i = 0; i < W; ++i) kw.w[i] = vw.w[i] = 0u;
-            }
-            float sc[W];
-            bool more = false;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                sc[i] = scale_of(vw.w[i]);
-                more |= sc[i] * c[i] >= 16384.f;
-            }
-            if (__any_sync(kFull, more)) raise(sc);
-            float* u = reinterpret_cast<float*>(un) + word;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                u[i] = scale_of(kw.w[i]);
-                u[16 * NG + i] = middle_of(kw.w[i]);
-                u[32 * NG + i] = sc[i] * c[i];
-                u[48 * NG + i] = middle_of(vw.w[i]);
-            }
-            __syncwarp();
-        }
+        const int rows[4] = {16 * sub + ra, 16 * sub + rb, 16 * sub + ra + 8, 16 * sub + rb + 8};
+        const int half = NG > 1 ? (g >> 2) * (4 * NGH) : 0;    // bytes to this lane half's middles
         // ---- logits
         float z[NT][4];
         {
             float ks[4][NG], km[4][NGH];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const Words<NG> w = lds<NG>(un + rows[e] * (4 * NG));
-                const Words<NGH> h = lds<NGH>(un + 64 * NG + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
+                const Words<NG> w = lds<NG>(un + U::KS + rows[e] * (4 * NG));
+                const Words<NGH> h = lds<NGH>(un + U::KM + rows[e] * (4 * NG) + half);
 #pragma unroll
                 for (int j = 0; j < NG; ++j) ks[e][j] = __uint_as_float(w.w[j]);
 #pragma unroll
@@ -393,7 +431,7 @@ struct Warp {
             constexpr float kOff = -129.f * 12582912.f;
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-                const Words<4> w = lds<4>(st + S::K + (8 * a + kr) * kRowCodes + 16 * t);
+                const Words<4> w = lds<4>(st + S::K + (16 * sub + 8 * a + kr) * kRowCodes + 16 * t);
                 int d[NT][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -425,9 +463,9 @@ struct Warp {
             if (valid != 0xffffu) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (!((valid >> rows[e]) & 1u)) z[nt][e] = -INFINITY;
+                    if (!((valid >> (rows[e] & 15)) & 1u)) z[nt][e] = -INFINITY;
             }
-            more |= fmaxf(fmaxf(z[nt][0], z[nt][1]), fmaxf(z[nt][2], z[nt][3])) > m[nt];
+            more |= fmaxf(fmaxf(z[nt][0], z[nt][1]), fmaxf(z[nt][2], z[nt][3])) + m[nt] > kMost;
         }
         // ---- a new maximum: sums down
         if (__any_sync(kFull, more)) {
@@ -436,7 +474,7 @@ struct Warp {
                 float mx = fmaxf(fmaxf(z[nt][0], z[nt][1]), fmaxf(z[nt][2], z[nt][3]));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-                const float mn = fmaxf(m[nt], mx), f = ex2(m[nt] - mn);
+                const float mn = fminf(m[nt], kRef - mx), f = ex2(mn - m[nt]);
                 m[nt] = mn;
                 l[nt] *= f;
 #pragma unroll
@@ -452,39 +490,44 @@ struct Warp {
                 }
             }
         }
-        // ---- weights, and their products with the scales
+        // ---- weights, and their products with the scales: this lane's column
+        // of B holds the first parts (g < 4) or the second ones.  With (a, b, d) =
+        // (p1, 0, 0) or (-p1, p1, p2), both are d s + (b s + fp16(a s)).
         uint32_t pb[NT][NG][2];
         {
-            const float second = g < 4 ? 0.f : 1.f;            // this lane's column: first or second part
-            float p[NT][4];
+            uint32_t wa[NT][2], wb[NT][2], wd[NT][2];
+            const uint32_t second = g < 4 ? 0u : 0xffffffffu;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[nt][e] = ex2(z[nt][e] - m[nt]);
-                l[nt] += (p[nt][0] + p[nt][1]) + (p[nt][2] + p[nt][3]);
+                for (int e = 0; e < 4; ++e) p[e] = ex2(z[nt][e] + m[nt]);
+                l[nt] += (p[0] + p[1]) + (p[2] + p[3]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t p1 = pack_f16(p[2 * k], p[2 * k + 1]);
+                    const float2 f = unpack_f16(p1);
+                    const uint32_t p2 = pack_f16(p[2 * k] - f.x, p[2 * k + 1] - f.y);
+                    wa[nt][k] = p1 ^ (second & 0x80008000u);
+                    wb[nt][k] = p1 & second;
+                    wd[nt][k] = p2 & second;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Words<NGH> h = lds<NGH>(un + U::VM + rows[e] * (4 * NG) + half);
+#pragma unroll
+                    for (int j = 0; j < NGH; ++j) Z[nt][j] = fmaf(p[e], __uint_as_float(h.w[j]), Z[nt][j]);
+                }
             }
-            float vs[4][NG];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Words<NG> w = lds<NG>(un + 128 * NG + rows[e] * (4 * NG));
-                const Words<NGH> h = lds<NGH>(un + 192 * NG + rows[e] * (4 * NG) + (NG > 1 ? (g >> 2) * (4 * NGH) : 0));
-#pragma unroll
-                for (int j = 0; j < NG; ++j) vs[e][j] = __uint_as_float(w.w[j]);
+            for (int k = 0; k < 2; ++k) {
+                const Words<NG> vs = lds<NG>(un + U::VS + (8 * sub + t + 4 * k) * (4 * NG));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < NGH; ++j) Z[nt][j] = fmaf(p[nt][e], __uint_as_float(h.w[j]), Z[nt][j]);
+                    for (int j = 0; j < NG; ++j)
+                        pb[nt][j][k] = fma2(wd[nt][k], vs.w[j], fma2(wb[nt][k], vs.w[j], mul2(wa[nt][k], vs.w[j])));
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float x0 = p[nt][2 * k] * vs[2 * k][j], x1 = p[nt][2 * k + 1] * vs[2 * k + 1][j];
-                        const float2 first = unpack_f16(pack_f16(x0, x1));
-                        pb[nt][j][k] = pack_f16(fmaf(-second, first.x, x0), fmaf(-second, first.y, x1));
-                    }
         }
         // ---- values: A is 16 channels x 16 rows
         Words<2> v[4];
@@ -518,7 +561,7 @@ struct Warp {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int J = 0; J < 4; ++J) {
-                const float inv = 1.f / __shfl_sync(kFull, c[J * NG / 4 % W], c_lane(J * NG / 4));
+                const float inv = 1.f / c[J * NG / 4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -532,7 +575,7 @@ struct Warp {
             s += __shfl_xor_sync(kFull, s, 1);
             s += __shfl_xor_sync(kFull, s, 2);
             float* r = red + (4 * nt + (g & 3)) * kRed + kD;
-            if (t == 0 && g < 4) { r[0] = m[nt]; r[1] = s; }
+            if (t == 0 && g < 4) { r[0] = -m[nt]; r[1] = s; }
 #pragma unroll
             for (int j = 0; j < NGH; ++j) {
                 float v = Z[nt][j];
@@ -732,38 +775,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
             const int64_t from = row0 + (ROWS ? 0 : (int64_t)first * kTile);
             const unsigned char* kc = a.K4.codes + (from + (ROWS ? 0 : r8)) * kRowCodes + 16 * ch;
             const unsigned char* vc = a.V4.codes + (from + (ROWS ? 0 : r8)) * kRowCodes + 16 * ch;
-            const uint32_t* par = (lane < 16 ? a.K4.params : a.V4.params) + (from + (ROWS ? 0 : lane & 15)) * NG;
+            const uint32_t* kp = a.K4.params + (from + (ROWS ? 0 : lane)) * NG;
+            const uint32_t* vp = a.V4.params + (from + (ROWS ? 0 : lane)) * NG;
             const uint32_t ring_at = smem_u32(ring);
             const uint32_t to_k = r8 * kRowCodes + 16 * ch, to_v = S::V + r8 * kRowCodes + 16 * (ch ^ ((r8 >> 1) & 2));
             const uint32_t to_p = S::KP + lane * (4 * NG);
-            // entry (lane % 16) of the warp's tile i: its position, -1 for none
-            auto entry = [&](int i) { return i < nb ? entry_row(a, x, u, (first + i * kWarps) * kTile + (lane & 15)) : -1; };
-            auto issue = [&](int i, int row) {
-                if (i < nb) {
-                    const uint32_t st = ring_at + (i % kStages) * S::bytes;
+            // entry `lane` of the warp's tile i: its position, -1 for none
+            auto entry = [&](int i) { return i < nb ? entry_row(a, x, u, (first + i * kWarps) * kTile + lane) : -1; };
+            // copies of the next tile to stage offset `to`, if there is one
+            int ahead = x.count - first * kTile;               // entries from that tile's first one on, if it is this warp's
+            int tiles_left = nb;
+            auto issue = [&](uint32_t to, int row) {
+                if (tiles_left > 0) {
+                    const uint32_t st = ring_at + to;
                     if (ROWS) {
-                        const uint32_t mask = __ballot_sync(kFull, row >= 0) & 0xffffu;
-                        row = max(row, 0);
-                        const int64_t k0 = (int64_t)__shfl_sync(kFull, row, r8) * kRowCodes;
-                        const int64_t k1 = (int64_t)__shfl_sync(kFull, row, r8 + 8) * kRowCodes;
-                        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + (i % kStages) * S::bytes + S::MASK) = mask;
-                        cp_async_bytes<16>(st + to_k, kc + k0);
-                        cp_async_bytes<16>(st + to_k + 8 * kRowCodes, kc + k1);
-                        cp_async_bytes<16>(st + to_v, vc + k0);
-                        cp_async_bytes<16>(st + to_v + 8 * kRowCodes, vc + k1);
-                        cp_async_bytes<4 * NG>(st + to_p, par + (int64_t)row * NG);
+                        const uint32_t mask = __ballot_sync(kFull, row >= 0);
+                        row = max(row, 0);                     // a row that is not there: row 0, which is never used
+                        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + to + S::MASK) = mask;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int64_t k = (int64_t)__shfl_sync(kFull, row, r8 + 8 * i) * kRowCodes;
+                            cp_async_bytes<16>(st + to_k + 8 * i * kRowCodes, kc + k);
+                            cp_async_bytes<16>(st + to_v + 8 * i * kRowCodes, vc + k);
+                        }
+                        cp_async_bytes<4 * NG>(st + to_p, kp + (int64_t)row * NG);
+                        cp_async_bytes<4 * NG>(st + to_p + kTile * 4 * NG, vp + (int64_t)row * NG);
                     } else {
-                        // the cache's rows are padded to whole tiles
-                        cp_async_bytes<16>(st + to_k, kc);
-                        cp_async_bytes<16>(st + to_k + 8 * kRowCodes, kc + 8 * kRowCodes);
-                        cp_async_bytes<16>(st + to_v, vc);
-                        cp_async_bytes<16>(st + to_v + 8 * kRowCodes, vc + 8 * kRowCodes);
-                        cp_async_bytes<4 * NG>(st + to_p, par);
+                        // rows behind the sequence are not read: the last tile may
+                        // reach past the end of the cache
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (r8 + 8 * i < ahead) {
+                                cp_async_bytes<16>(st + to_k + 8 * i * kRowCodes, kc + 8 * i * kRowCodes);
+                                cp_async_bytes<16>(st + to_v + 8 * i * kRowCodes, vc + 8 * i * kRowCodes);
+                            }
+                        if (lane < ahead) {
+                            cp_async_bytes<4 * NG>(st + to_p, kp);
+                            cp_async_bytes<4 * NG>(st + to_p + kTile * 4 * NG, vp);
+                        }
                         kc += kWarps * kTile * kRowCodes;
                         vc += kWarps * kTile * kRowCodes;
-                        par += kWarps * kTile * NG;
+                        kp += kWarps * kTile * NG;
+                        vp += kWarps * kTile * NG;
                     }
                 }
+                ahead -= kWarps * kTile;
+                --tiles_left;
                 cp_async_commit();
             };
             int row = 0;
@@ -772,27 +829,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
             for (int i = 0; i < kStages - 1; ++i) {
                 const int now = row;
                 if (ROWS) row = entry(i + 1);
-                issue(i, now);
+                issue(i * S::bytes, now);
             }
             Warp<NG, NT> w;
             w.start(a, x, bf16 != 0);
+            // the rows of the tile at stage offset `at`; left: entries from its first one on
+            auto valid_of = [&](uint32_t at, int left) -> uint32_t {
+                if (ROWS) return *reinterpret_cast<const uint32_t*>(ring + at + S::MASK);
+                return left < kTile ? (1u << left) - 1u : 0xffffffffu;
+            };
+            int left = x.count - first * kTile;
+            uint32_t cur = 0u;
+            unsigned char* un = ring + kStages * S::bytes;
             for (int i = 0; i < nb; ++i) {
+                // this tile's copies have arrived and are seen by the warp
+                cp_async_wait<kStages - 2>();
+                __syncwarp();
+                const uint32_t valid = valid_of(cur, left);
                 const int now = row;
                 if (ROWS) row = entry(i + kStages);
-                issue(i + kStages - 1, now);
-                cp_async_wait<kStages - 1>();
+                issue(S::bytes - cur, now);                    // into the other stage, read by the tile before
+                w.unpack(ring + cur, un, valid);
                 __syncwarp();
-                const unsigned char* st = ring + (i % kStages) * S::bytes;
-                uint32_t valid = 0xffffu;
-                if (ROWS) {
-                    valid = *reinterpret_cast<const uint32_t*>(st + S::MASK);
-                } else {
-                    const int left = x.count - (first + i * kWarps) * kTile;
-                    if (left < kTile) valid = (1u << left) - 1u;
-                }
-                w.tile(st, ring + kStages * S::bytes, valid);
-                __syncwarp();
+                w.rows16(ring + cur, un, 0, valid & 0xffffu);
+                if (valid >> 16) w.rows16(ring + cur, un, 1, valid >> 16);
+                cur = S::bytes - cur;
+                left -= kWarps * kTile;
             }
+            static_assert(kStages == 2, "cur alternates between two stages");
             cp_async_wait<0>();
             __syncwarp();
             w.finish(reinterpret_cast<float*>(ring));          // the ring is drained
