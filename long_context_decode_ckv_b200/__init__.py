@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # CKV_DEBUG_BOUNDS=1 in the environment selects the range-checked build
@@ -134,7 +135,7 @@ def lib() -> ctypes.CDLL:
     L.ckv_kv4_workspace.restype = sz
     L.ckv_kv4_workspace.argtypes = [C]
     L.ckv_qk_norm_rope.restype = st
-    L.ckv_qk_norm_rope.argtypes = [C, ctypes.POINTER(ckv_qkv), P]
+    L.ckv_qk_norm_rope.argtypes = [C, P, P]                     # a ckv_qkv, or its bytes
     L.ckv_kv4_write.restype = st
     L.ckv_kv4_write.argtypes = [C, I, P, P, P, P, I, P, P, P, P]
     L.ckv_kv4_read.restype = st
@@ -381,7 +382,9 @@ def ckv_dense_decode(ctx, q, K, V, n, out, lse=None, stream=None):
 
 
 # ----------------------------------------- rows into the caches, 4-bit caches
-_I3 = ctypes.c_int64 * 3
+# These calls run once per layer and token, so what they check of their
+# tensors is one expression of attribute reads; _refuse then says what is wrong.
+_qkv_bytes = struct.Struct("@4i2f4P9q4P3q4P")                      # ckv_qkv
 
 
 def _dtypes():
@@ -396,7 +399,9 @@ def _dtypes():
 _dtypes_known = None
 
 
-def _refuse(what, device, x):
+def _refuse(device, x, what):
+    if x is None or isinstance(x, int) or not hasattr(x, "get_device"):
+        raise TypeError(f"expected {what} on device {device}, got {type(x).__name__}")
     _dev(x)                                                        # host memory: TypeError
     raise ValueError(f"expected {what} on device {device}, got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on "
                      f"{x.device}")
@@ -407,33 +412,37 @@ def _on(device, x, dtype, shape):
     `shape` on `device`, a raw int address or None."""
     if x is None or x.__class__ is int:
         return x
-    if not hasattr(x, "get_device") or x.get_device() != device or x.dtype is not dtype or x.shape != shape or \
-            not x.is_contiguous():
-        _refuse(f"a contiguous {dtype} tensor of shape {tuple(shape)}", device, x)
-    return x.data_ptr()
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == device and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(device, x, f"a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
 def _buffer(device, x, size):
     """Address of a byte buffer (a 4-bit cache, a workspace) of at least `size` bytes."""
     if x is None or x.__class__ is int:
         return x
-    if not hasattr(x, "get_device") or x.get_device() != device or x.numel() * x.element_size() < size or \
-            not x.is_contiguous():
-        _refuse(f"a contiguous buffer of {size} bytes", device, x)
-    return x.data_ptr()
+    try:
+        if x.get_device() == device and x.nbytes >= size and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(device, x, f"a contiguous buffer of {size} bytes")
 
 
 def _rows4(device, x, dtype, shape):
-    """Address and (batch, token, head) strides of rows [B][T][heads][D]: a
-    CUDA tensor of that shape, its channels contiguous."""
-    if not hasattr(x, "get_device") or x.get_device() != device or x.dtype is not dtype or x.shape != shape:
-        if x is None or isinstance(x, int):
-            raise TypeError("expected a CUDA tensor of rows")
-        _refuse(f"{dtype} rows of shape {tuple(shape)}", device, x)
-    batch, token, head, channel = x.stride()
-    if channel != 1:
-        _refuse(f"{dtype} rows with contiguous channels", device, x)
-    return x.data_ptr(), _I3(batch, token, head)
+    """Address and strides of rows [B][T][heads][D]: a CUDA tensor of that
+    shape, its channels contiguous."""
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == device:
+            strides = x.stride()
+            if strides[3] == 1:
+                return x.data_ptr(), strides
+    except AttributeError:
+        pass
+    _refuse(device, x, f"{dtype} rows of shape {tuple(shape)} with contiguous channels")
 
 
 def ckv_kv4_bytes(cfg, group) -> int:
@@ -450,73 +459,100 @@ def ckv_qk_norm_rope(cfg, q, k, v, pos, q_out, inv_freq_host, *, q_weight=None, 
     CUDA tensors [B][T][heads][D] with any (batch, token, head) strides;
     inv_freq_host is a host array of rot_dim / 2 float64 frequencies (None: no
     rotation)."""
-    L, (i32, _, elems) = lib(), _dtypes()
+    L, (i32, _, elems), c = _lib or lib(), _dtypes_known or _dtypes(), ctypes.byref(cfg)
     B, Hq, Hkv, D, dev = cfg.batch, cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.device
     elem = elems[cfg.kv_dtype]
     T = k.shape[1]
     rot, freq = 0, None
     if inv_freq_host is not None:
         freq, rot = _hostp(inv_freq_host), 2 * len(inv_freq_host)
-        if str(inv_freq_host.dtype)[-7:] != "float64" or inv_freq_host.ndim != 1 or \
+        if inv_freq_host.dtype not in _float64() or inv_freq_host.ndim != 1 or \
                 not (inv_freq_host.is_contiguous() if hasattr(inv_freq_host, "is_contiguous")
                      else inv_freq_host.flags["C_CONTIGUOUS"]):
             raise TypeError("expected a contiguous float64 array of frequencies")
-    qp, qs = _rows4(dev, q, elem, (B, T, Hq, D))
-    kp, ks = _rows4(dev, k, elem, (B, T, Hkv, D))
-    vp, vs = _rows4(dev, v, elem, (B, T, Hkv, D))
-    op, os_ = _rows4(dev, q_out, elem, (B, T, Hq, D))
-    cache = (B, Hkv, cfg.n_max, D)
-    size = L.ckv_kv4_bytes(ctypes.byref(cfg), group) if K4 is not None or V4 is not None else 0
-    x = ckv_qkv(T, rot, bool(interleaved), group, eps, rot_scale, freq, qp, kp, vp, qs, ks, vs, _on(dev, pos, i32, (B, T)),
-                _on(dev, q_weight, elem, (D,)), _on(dev, k_weight, elem, (D,)), op, os_, _on(dev, K, elem, cache),
-                _on(dev, V, elem, cache), _buffer(dev, K4, size), _buffer(dev, V4, size))
-    _check("ckv_qk_norm_rope", L.ckv_qk_norm_rope(ctypes.byref(cfg), ctypes.byref(x), _stream(stream)))
+    rows, heads = (B, T, Hq, D), (B, T, Hkv, D)
+    qp, (q0, q1, q2, _) = _rows4(dev, q, elem, rows)
+    kp, (k0, k1, k2, _) = _rows4(dev, k, elem, heads)
+    vp, (v0, v1, v2, _) = _rows4(dev, v, elem, heads)
+    op, (o0, o1, o2, _) = _rows4(dev, q_out, elem, rows)
+    cache, vec = (B, Hkv, cfg.n_max, D), (D,)
+    size = L.ckv_kv4_bytes(c, group) if K4 is not None or V4 is not None else 0
+    x = _qkv_bytes.pack(
+        T, rot, bool(interleaved), group, eps, rot_scale, freq or 0, qp, kp, vp, q0, q1, q2, k0, k1, k2, v0, v1, v2,
+        _on(dev, pos, i32, (B, T)) or 0, _on(dev, q_weight, elem, vec) or 0, _on(dev, k_weight, elem, vec) or 0, op, o0, o1, o2,
+        _on(dev, K, elem, cache) or 0, _on(dev, V, elem, cache) or 0, _buffer(dev, K4, size) or 0, _buffer(dev, V4, size) or 0)
+    status = L.ckv_qk_norm_rope(c, x, _stream(stream))
+    if status:
+        raise CkvError("ckv_qk_norm_rope", status)
+
+
+def _float64():
+    global _float64_known
+    if _float64_known is None:
+        import numpy as np
+        import torch
+        _float64_known = torch.float64, np.dtype(np.float64)
+    return _float64_known
+
+
+_float64_known = None
 
 
 def ckv_kv4_write(cfg, group, k, v, pos, K4, V4, stream=None):
     """Rows k, v (CUDA tensors [B][T][H_kv][D], any strides) into the 4-bit
     caches at pos [B][T] (None: 0 .. T-1)."""
-    L, (i32, _, elems), c = lib(), _dtypes(), ctypes.byref(cfg)
+    L, (i32, _, elems), c = _lib or lib(), _dtypes_known or _dtypes(), ctypes.byref(cfg)
     dev, T, elem = cfg.device, k.shape[1], elems[cfg.kv_dtype]
     shape = (cfg.batch, T, cfg.n_kv_heads, cfg.head_dim)
     kp, ks = _rows4(dev, k, elem, shape)
     vp, vs = _rows4(dev, v, elem, shape)
     size = L.ckv_kv4_bytes(c, group)
-    _check("ckv_kv4_write", L.ckv_kv4_write(c, group, kp, ks, vp, vs, T, _on(dev, pos, i32, shape[:2]),
-                                            _buffer(dev, K4, size), _buffer(dev, V4, size), _stream(stream)))
+    status = L.ckv_kv4_write(c, group, kp, _int64x3.pack(*ks[:3]), vp, _int64x3.pack(*vs[:3]), T, _on(dev, pos, i32, shape[:2]),
+                             _buffer(dev, K4, size), _buffer(dev, V4, size), _stream(stream))
+    if status:
+        raise CkvError("ckv_kv4_write", status)
+
+
+_int64x3 = struct.Struct("@3q")
 
 
 def ckv_kv4_read(cfg, group, K4, V4, first, count, K, V, stream=None):
     """Rows [first, first + count) of the 4-bit caches into the same rows of K and V."""
-    L, c, dev, elem = lib(), ctypes.byref(cfg), cfg.device, _dtypes()[2][cfg.kv_dtype]
+    L, c, dev, elem = _lib or lib(), ctypes.byref(cfg), cfg.device, (_dtypes_known or _dtypes())[2][cfg.kv_dtype]
     size = L.ckv_kv4_bytes(c, group)
     cache = (cfg.batch, cfg.n_kv_heads, cfg.n_max, cfg.head_dim)
-    _check("ckv_kv4_read", L.ckv_kv4_read(c, group, _buffer(dev, K4, size), _buffer(dev, V4, size), first, count,
-                                          _on(dev, K, elem, cache), _on(dev, V, elem, cache), _stream(stream)))
+    status = L.ckv_kv4_read(c, group, _buffer(dev, K4, size), _buffer(dev, V4, size), first, count, _on(dev, K, elem, cache),
+                            _on(dev, V, elem, cache), _stream(stream))
+    if status:
+        raise CkvError("ckv_kv4_read", status)
 
 
 def ckv_kv4_dense_decode(cfg, group, q, K4, V4, n, lens, workspace, out, lse=None, stream=None):
     """Dense decode attention over 4-bit caches: positions [0, lens[b]) (None: [0, n))."""
-    L, (i32, f32, elems), c = lib(), _dtypes(), ctypes.byref(cfg)
-    dev, heads = cfg.device, (cfg.batch, cfg.n_q_heads)
-    rows, size = heads + (cfg.head_dim,), L.ckv_kv4_bytes(c, group)
-    _check("ckv_kv4_dense_decode", L.ckv_kv4_dense_decode(
+    L, (i32, f32, elems), c = _lib or lib(), _dtypes_known or _dtypes(), ctypes.byref(cfg)
+    B, Hq, dev = cfg.batch, cfg.n_q_heads, cfg.device
+    rows, size = (B, Hq, cfg.head_dim), L.ckv_kv4_bytes(c, group)
+    status = L.ckv_kv4_dense_decode(
         c, group, _on(dev, q, elems[cfg.kv_dtype], rows), _buffer(dev, K4, size), _buffer(dev, V4, size), n,
-        _on(dev, lens, i32, heads[:1]), _buffer(dev, workspace, L.ckv_kv4_workspace(c)), _on(dev, out, f32, rows),
-        _on(dev, lse, f32, heads), _stream(stream)))
+        _on(dev, lens, i32, (B,)), _buffer(dev, workspace, L.ckv_kv4_workspace(c)), _on(dev, out, f32, rows),
+        _on(dev, lse, f32, (B, Hq)), _stream(stream))
+    if status:
+        raise CkvError("ckv_kv4_dense_decode", status)
 
 
 def ckv_kv4_attend_rows(cfg, group, q, K4, V4, n, lens, rows, n_rows, max_rows, workspace, out, lse=None, stream=None):
     """Decode attention over the sinks, rows[g][0 .. n_rows[g]) and the new token of 4-bit caches."""
-    L, (i32, f32, elems), c = lib(), _dtypes(), ctypes.byref(cfg)
-    dev, heads = cfg.device, (cfg.batch, cfg.n_q_heads)
-    shape, size = heads + (cfg.head_dim,), L.ckv_kv4_bytes(c, group)
-    graphs = cfg.batch * (cfg.n_q_heads if cfg.mode == CKV_PER_HEAD else cfg.n_kv_heads)
-    _check("ckv_kv4_attend_rows", L.ckv_kv4_attend_rows(
+    L, (i32, f32, elems), c = _lib or lib(), _dtypes_known or _dtypes(), ctypes.byref(cfg)
+    B, Hq, dev = cfg.batch, cfg.n_q_heads, cfg.device
+    shape, size = (B, Hq, cfg.head_dim), L.ckv_kv4_bytes(c, group)
+    graphs = B * (Hq if cfg.mode == CKV_PER_HEAD else cfg.n_kv_heads)
+    status = L.ckv_kv4_attend_rows(
         c, group, _on(dev, q, elems[cfg.kv_dtype], shape), _buffer(dev, K4, size), _buffer(dev, V4, size), n,
-        _on(dev, lens, i32, heads[:1]), _on(dev, rows, i32, (graphs, max_rows)), _on(dev, n_rows, i32, (graphs,)),
-        max_rows, _buffer(dev, workspace, L.ckv_kv4_workspace(c)), _on(dev, out, f32, shape), _on(dev, lse, f32, heads),
-        _stream(stream)))
+        _on(dev, lens, i32, (B,)), _on(dev, rows, i32, (graphs, max_rows)), _on(dev, n_rows, i32, (graphs,)), max_rows,
+        _buffer(dev, workspace, L.ckv_kv4_workspace(c)), _on(dev, out, f32, shape), _on(dev, lse, f32, (B, Hq)),
+        _stream(stream))
+    if status:
+        raise CkvError("ckv_kv4_attend_rows", status)
 
 
 def ckv_debug_poke(ctx, what: int, g: int, c: int, r: int, value: int):

@@ -6,7 +6,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <mutex>
+#include <atomic>
 
 #include "device_guard.h"
 #include "kv4.cuh"
@@ -34,16 +34,15 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 // multiprocessors of a device; looked up once per device
 ckv_status device_sms(int device, int* sms)
 {
-    static std::mutex mutex;
-    static int known[kMaxDevices];
-    std::lock_guard<std::mutex> lock(mutex);
-    if (!known[device]) {
-        int count = 0, n = 0;
+    static std::atomic<int> known[kMaxDevices];
+    int n = known[device].load(std::memory_order_relaxed);
+    if (!n) {
+        int count = 0;
         if (cudaGetDeviceCount(&count) != cudaSuccess || device >= count) return CKV_ERR_INVALID_ARG;
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return CKV_ERR_CUDA;
-        known[device] = n;
+        known[device].store(n, std::memory_order_relaxed);
     }
-    *sms = known[device];
+    *sms = n;
     return CKV_OK;
 }
 
@@ -102,6 +101,7 @@ ckv_status attend(const ckv_config* cfg, int group, const void* q, const void* K
     a.U = cfg->batch * cfg->n_q_heads / NH;
     a.n = n;
     a.group = group;
+    a.device = cfg->device;
     a.lens = lens;
     if (listed) {
         // without a list the kernel still needs a non-null pointer to know the mode

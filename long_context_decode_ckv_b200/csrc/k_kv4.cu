@@ -35,6 +35,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kv4.cuh"
 #include "warp_mma.cuh"
 
@@ -630,11 +632,14 @@ __device__ __forceinline__ void merge_slots(const Kv4AttendArgs& a, const Unit& 
     const float4* so = reinterpret_cast<const float4*>(a.part + (int64_t)(u + pf) * a.NH * kD);
     for (int h = warp; h < a.NH; h += kWarps) {
         float M = -FLT_MAX, L = 0.f;
-        for (int s = lane; s < ns; s += 32) M = fmaxf(M, __ldcg(sm + (int64_t)s * a.NH + h).x);
+        float2 v = make_float2(-FLT_MAX, 0.f);             // this lane's first slot
+        if (lane < ns) v = __ldcg(sm + (int64_t)lane * a.NH + h);
+        M = v.x;
+        for (int s = lane + 32; s < ns; s += 32) M = fmaxf(M, __ldcg(sm + (int64_t)s * a.NH + h).x);
 #pragma unroll
         for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
         for (int s = lane; s < ns; s += 32) {
-            const float2 v = __ldcg(sm + (int64_t)s * a.NH + h);
+            if (s >= 32) v = __ldcg(sm + (int64_t)s * a.NH + h);
             const float f = part_weight(v.x, v.y, M);
             weight[h * ns + s] = f;
             L += f * v.y;
@@ -879,13 +884,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
                 so[i] = merge_warps<NG>(red, kRedWarp, i / kD, i % kD, M, L);
                 if (i % kD == 0) sm[i / kD] = make_float2(M, L);
             }
-            __threadfence();
+            // ---- arrival; the unit's last piece merges every slot.  The
+            // barrier orders the CTA's stores before thread 0's fence, which
+            // makes them visible before its arrival; likewise the other way.
             __syncthreads();
-            // ---- arrival; the unit's last piece merges every slot
-            if (tid == 0) s_last = atomicAdd(a.cnt + u, 1u) == (unsigned)(pl - pf);
+            if (tid == 0) {
+                __threadfence();
+                s_last = atomicAdd(a.cnt + u, 1u) == (unsigned)(pl - pf);
+                __threadfence();
+            }
             __syncthreads();
             if (s_last) {
-                __threadfence();
                 merge_slots(a, x, u, pf, pl - pf + 1, red);
                 if (tid == 0) a.cnt[u] = 0;
             }
@@ -900,13 +909,26 @@ template <int NG, int NT, bool ROWS>
 cudaError_t launch_attend_t(const Kv4AttendArgs& a, int bf16, int sms, cudaStream_t st)
 {
     auto fn = k_kv4_attend<NG, NT, ROWS>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kWarpSmem<NG>);
-    if (e != cudaSuccess) return e;
-    long long tiles = ROWS ? ((long long)a.S + a.max_rows + 1 + kTile - 1) / kTile : (a.n + kTile - 1) / kTile;
-    tiles *= a.U;
-    long long P = (tiles + kWarps - 1) / kWarps;
-    P = P < (long long)kCtasPerSM<NT> * sms ? P : (long long)kCtasPerSM<NT> * sms;
-    P = P < kKv4MaxCtas ? P : kKv4MaxCtas;
+    static std::atomic<uint64_t> prepared{0};              // devices (bit = ordinal) that know the kernel's shared memory
+    if (!(prepared.load(std::memory_order_acquire) >> a.device & 1)) {
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kWarpSmem<NG>);
+        if (e != cudaSuccess) return e;
+        prepared.fetch_or(uint64_t(1) << a.device, std::memory_order_release);
+    }
+    // tiles of a unit, at most
+    const long long tiles = ROWS ? ((long long)a.S + a.max_rows + 1 + kTile - 1) / kTile : (a.n + kTile - 1) / kTile;
+    const long long most = kCtasPerSM<NT> * sms < kKv4MaxCtas ? kCtasPerSM<NT> * sms : kKv4MaxCtas;
+    // Few tiles: shares that start and end with units (where all are as long
+    // as the longest), a CTA for each unit while a warp has up to 3 tiles; a
+    // merge through slots costs about as much as two more tiles.  Many
+    // tiles: the whole machine, wherever the shares' borders fall.
+    long long P = (long long)a.U * tiles;
+    if (P > most * kWarps * 4) P = most;
+    else {
+        const long long each = tiles <= 3 * kWarps ? 1 : (tiles + kWarps - 1) / kWarps;
+        P = a.U * each;
+        if (P > most) P = a.U < most ? most / a.U * a.U : most;
+    }
     fn<<<(unsigned)P, kThreads, kWarps * kWarpSmem<NG>, st>>>(a, bf16);
     return cudaGetLastError();
 }

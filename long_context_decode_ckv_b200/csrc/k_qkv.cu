@@ -326,20 +326,21 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8])
 #pragma unroll
         for (int i = 1; i < 4; ++i) s[k] = __fadd_rn(s[k], __fmul_rn(x[4 * k + i], x[4 * k + i]));
     }
-    if (SPLIT) {
+    if constexpr (SPLIT) {
         // sums l and l + 16 are this lane's
         float t = __fadd_rn(s[0], s[1]);
 #pragma unroll
         for (int off = 8; off; off >>= 1) t = __fadd_rn(t, __shfl_xor_sync(kAll, t, off));
         return t;
-    }
-    // sums 2 l and 2 l + 1
+    } else {
+        // sums 2 l and 2 l + 1
 #pragma unroll
-    for (int off = 8; off; off >>= 1) {
-        s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], off));
-        s[1] = __fadd_rn(s[1], __shfl_xor_sync(kAll, s[1], off));
+        for (int off = 8; off; off >>= 1) {
+            s[0] = __fadd_rn(s[0], __shfl_xor_sync(kAll, s[0], off));
+            s[1] = __fadd_rn(s[1], __shfl_xor_sync(kAll, s[1], off));
+        }
+        return __fadd_rn(s[0], s[1]);
     }
-    return __fadd_rn(s[0], s[1]);
 }
 
 // The rotation of a lane's channels: x[e] c[e] + partner s[e], s with its sign.
@@ -408,7 +409,9 @@ struct Rotation {
 enum { kQuery = 0, kKey = 1, kValue = 2 };
 
 // A warp: heads [h0, h1) of one token's queries, keys or values, two at a
-// time (16 lanes a row), the next two loaded before these are worked on.
+// time (16 lanes a row), with kAhead loads under way: 24 warps an SM times 3
+// times 512 bytes cover the latency of the memory, which one load a warp did
+// not (16384 tokens of 32 + 16 heads: 97 us).
 // Rows that are not quantised are held split, where a pair (i, i + 64) is one
 // lane's; a group of a quantised row lies in few lanes only if they are whole.
 template <bool BF16, int KIND, int GROUP>
@@ -422,8 +425,13 @@ __device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos,
     const void* weight = KIND == kQuery ? a.q_weight : KIND == kKey ? a.k_weight : nullptr;
     const char* from = static_cast<const char*>(src.data) + (b * src.batch + t * src.token + (h0 + half) * src.head + R::at(l)) * ESZ;
     const int64_t step = 2 * src.head * ESZ;
-    R next;
-    if (h0 + half < h1) next.load(from, 0);
+    constexpr int kAhead = GROUP ? 1 : BF16 ? 3 : 2;
+    R next[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        if (h0 + half + 2 * i < h1) next[i].load(from, 0);
+        from += step;
+    }
     // where the row goes: q_out, or the cache's row of this position
     const int64_t unit0 = (int64_t)b * a.Hkv + h0 + half;
     char* to = static_cast<char*>(KIND == kQuery ? a.q_out : KIND == kKey ? a.K : a.V);
@@ -445,41 +453,46 @@ __device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos,
         }
         if (rot) turn.make(a, turns);
     }
-    for (int left = h1 - h0; left > 0; left -= 2) {
-        R raw = next;
-        const bool live = half < left;
-        from += step;
-        if (half + 2 < left) next.load(from, 0);
-        float x[8];
-        if (KIND != kValue || GROUP) raw.floats(x);
-        if (KIND != kValue) {
-            if (weight) {
-                const float r = rsqrtf(fmaf(sum_squares<SPLIT>(x), 1.f / kD, eps));
+    for (int left = h1 - h0; left > 0;) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * f[i];
+        for (int i = 0; i < kAhead; ++i) {
+            if (left <= 0) break;
+            R raw = next[i];
+            const bool live = half < left;
+            if (half + 2 * kAhead < left) next[i].load(from, 0);
+            from += step;
+            float x[8];
+            if (KIND != kValue || GROUP) raw.floats(x);
+            if (KIND != kValue) {
+                if (weight) {
+                    const float r = rsqrtf(fmaf(sum_squares<SPLIT>(x), 1.f / kD, eps));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * f[e];
+                }
+                if (rot) turn.apply(a, x);
+                raw.set(x);
             }
-            if (rot) turn.apply(a, x);
-            raw.set(x);
-        }
-        if (plain) {
-            if (live) raw.store(to, 0);
-            to += to_step;
-        }
-        if constexpr (GROUP != 0 && KIND != kQuery) {
-            if (KIND == kKey) raw.floats(x);               // as the cache rounds them
-            float lo, hi;
-            uint32_t params, code[2];
-            raw.template extremes<GROUP>(x, lo, hi);
-            kv4_quantise<BF16, KIND == kValue>(x, lo, hi, params, code);
-            if (live) kv4_store<GROUP, KIND == kValue>(four, row4, l, code, params);
-            row4 += 2 * four.R;
+            if (plain) {
+                if (live) raw.store(to, 0);
+                to += to_step;
+            }
+            if constexpr (GROUP != 0 && KIND != kQuery) {
+                if (KIND == kKey) raw.floats(x);           // as the cache rounds them
+                float lo, hi;
+                uint32_t params, code[2];
+                raw.template extremes<GROUP>(x, lo, hi);
+                kv4_quantise<BF16, KIND == kValue>(x, lo, hi, params, code);
+                if (live) kv4_store<GROUP, KIND == kValue>(four, row4, l, code, params);
+                row4 += 2 * four.R;
+            }
+            left -= 2;
         }
     }
 }
 
 // One warp: rows [r0, r1) of one token, q heads, then k heads, then v heads.
 template <bool BF16, int GROUP>
-__global__ void __launch_bounds__(32 * kQkvWarps, GROUP ? 6 : 8) k_qkv(const __grid_constant__ QkvArgs a, int per_warp, int slices)
+__global__ void __launch_bounds__(32 * kQkvWarps, 6) k_qkv(const __grid_constant__ QkvArgs a, int per_warp, int slices)
 {
     const int64_t w = (int64_t)blockIdx.x * kQkvWarps + (threadIdx.x >> 5);
     const int token = (int)(w / slices);

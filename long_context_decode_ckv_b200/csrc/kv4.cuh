@@ -84,6 +84,7 @@ struct Kv4AttendArgs {
     int U, NH;                       // units (lists of rows) and query heads of each
     int n;                           // most positions of a sequence
     int group;
+    int device;                      // ordinal, below 64
     const int32_t* lens;             // [B], or null: n for every sequence
     const int32_t* rows;             // [U][max_rows], or null: dense
     const int32_t* n_rows;           // [U]
