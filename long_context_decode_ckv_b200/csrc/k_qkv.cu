@@ -12,10 +12,12 @@
 // its cosine and sine are rounded once, since a 32-bit angle at position
 // 131072 would be off by up to 2^-8 radians.
 //
-// 16 lanes hold one row, 8 channels each (one 16-byte load of bfloat16); a
-// warp holds two rows at a time and walks the rows of its share of one token,
-// so the token's angles are formed once.  Memory bound: (Hq + 2 Hkv) rows
-// read and written once per token.
+// 16 lanes hold one row, 8 channels each; a warp holds two rows at a time and
+// walks its share of one token's rows.  Memory bound where nothing is
+// quantised: (Hq + 2 Hkv) rows read and written once per token (16384 tokens
+// of 32 + 16 heads, 403 MB: 86 us, 4.7 TB/s; without norm and rotation 74 us,
+// a plain copy of as much 62 us).  Quantised rows are bound by instructions,
+// about 200 for two rows (16384 x 16 rows to groups of 32: 36 us, 2.5 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -280,8 +282,26 @@ struct Raw {
     }
 };
 
-// A token's cosines and sines: lane i has those of pairs i and i + 32, formed
-// in 64 bits and rounded once.
+// Cosine and sine of t revolutions in 64 bits, rounded once: t less the
+// nearest quarter, then the Taylor series to the 14th and 15th power of the
+// angle, at most pi / 4 (the next terms are below 2^-49).
+__device__ __forceinline__ void turn_by(double t, float& c, float& s)
+{
+    t -= rint(t);
+    const double quarter = rint(4.0 * t);
+    const double x = (t - 0.25 * quarter) * 6.283185307179586476925286766559, z = x * x;
+    const double sn = x * fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, -1.0 / 1307674368000.0 * z + 1.0 / 6227020800.0,
+                      -1.0 / 39916800.0), 1.0 / 362880.0), -1.0 / 5040.0), 1.0 / 120.0), -1.0 / 6.0), 1.0);
+    const double cs = fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, -1.0 / 87178291200.0, 1.0 / 479001600.0),
+                      -1.0 / 3628800.0), 1.0 / 40320.0), -1.0 / 720.0), 1.0 / 24.0), -0.5), 1.0);
+    const int q = (int)quarter & 3;
+    const float a = (float)(q & 1 ? sn : cs), b = (float)(q & 1 ? cs : sn);
+    c = q == 1 || q == 2 ? -a : a;
+    s = q >= 2 ? -b : b;
+}
+
+// A token's cosines and sines: lane (l, half) = (lane % 16, lane / 16) has
+// those of pairs 4 l + 2 half and + 1.
 struct Turns {
     float c[2], s[2];
     __device__ __forceinline__ Turns(const QkvArgs& a, int pos)
@@ -289,25 +309,24 @@ struct Turns {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int i = lane + 32 * k;
+            const int i = 4 * (lane & 15) + 2 * (lane >> 4) + k;
             c[k] = 1.f;
             s[k] = 0.f;
             if (i < a.rot / 2) {
-                const double t = (double)pos * a.turn[i];
-                double sn, cs;
-                sincospi(2.0 * (t - rint(t)), &sn, &cs);
-                c[k] = (float)cs * a.rot_scale;
-                s[k] = (float)sn * a.rot_scale;
+                turn_by((double)pos * a.turn[i], c[k], s[k]);
+                c[k] *= a.rot_scale;
+                s[k] *= a.rot_scale;
             }
         }
     }
     // those of pair i; all lanes call
     __device__ __forceinline__ void of(int i, float& ci, float& si) const
     {
-        const float c0 = __shfl_sync(kAll, c[0], i & 31), c1 = __shfl_sync(kAll, c[1], i & 31);
-        const float s0 = __shfl_sync(kAll, s[0], i & 31), s1 = __shfl_sync(kAll, s[1], i & 31);
-        ci = i & 32 ? c1 : c0;
-        si = i & 32 ? s1 : s0;
+        const int from = (i >> 2) + 8 * (i & 2);
+        const float c0 = __shfl_sync(kAll, c[0], from), c1 = __shfl_sync(kAll, c[1], from);
+        const float s0 = __shfl_sync(kAll, s[0], from), s1 = __shfl_sync(kAll, s[1], from);
+        ci = i & 1 ? c1 : c0;
+        si = i & 1 ? s1 : s0;
     }
 };
 
@@ -347,41 +366,32 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8])
 // Products and sums are rounded one by one, as the formula has them.
 template <bool SPLIT>
 struct Rotation {
-    float c[8], s[8];        // split and 128 rotated, or interleaved: of the lane's 4 pairs, in [0, 4)
+    float c[8], s[8];        // interleaved: of the lane's 4 pairs, in [0, 4)
 
-    __device__ __forceinline__ void make(const QkvArgs& a, const Turns& turns)
+    static __device__ __forceinline__ int channel(int l, int e) { return SPLIT ? (e < 4 ? 4 * l + e : 60 + 4 * l + e) : 8 * l + e; }
+    __device__ __forceinline__ void make(const QkvArgs& a, int pos)
     {
+        const Turns turns(a, pos);
         const int l = threadIdx.x & 15, half = a.rot / 2;
-        const bool four = a.interleaved || (SPLIT && a.rot == kD);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (four && e >= 4) break;
-            const int ch = channel(l, four && a.interleaved ? 2 * e : e);
+            if (a.interleaved && e >= 4) break;
+            const int ch = channel(l, a.interleaved ? 2 * e : e);
             const int pair = a.interleaved ? ch / 2 : ch < half ? ch : ch - half;
             turns.of(pair & 63, c[e], s[e]);
-            if (!four && ch < half) s[e] = -s[e];
+            if (!a.interleaved && ch < half) s[e] = -s[e];
             if (ch >= a.rot) { c[e] = 1.f; s[e] = 0.f; }
         }
     }
-    static __device__ __forceinline__ int channel(int l, int e) { return SPLIT ? (e < 4 ? 4 * l + e : 60 + 4 * l + e) : 8 * l + e; }
-
     // all lanes call
     __device__ __forceinline__ void apply(const QkvArgs& a, float (&x)[8]) const
     {
-        if (a.interleaved || (SPLIT && a.rot == kD)) {
+        if (a.interleaved) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // the pair (2 i, 2 i + 1) of the lane, or (i, i + 4): channels 4 l + i and 64 + 4 l + i
-                const int p0 = 2 * i, p1 = 2 * i + 1;
-                if (a.interleaved) {
-                    const float u = x[p0], v = x[p1];
-                    x[p0] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(v, s[i]));
-                    x[p1] = __fadd_rn(__fmul_rn(v, c[i]), __fmul_rn(u, s[i]));
-                } else {
-                    const float u = x[i], v = x[i + 4];
-                    x[i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(v, s[i]));
-                    x[i + 4] = __fadd_rn(__fmul_rn(v, c[i]), __fmul_rn(u, s[i]));
-                }
+                const float u = x[2 * i], v = x[2 * i + 1];
+                x[2 * i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(v, s[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(v, c[i]), __fmul_rn(u, s[i]));
             }
             return;
         }
@@ -405,71 +415,92 @@ struct Rotation {
         for (int e = 0; e < 8; ++e) x[e] = y[e];
     }
 };
+// All 128 channels in pairs (i, i + 64) of split rows: both are the lane's.
+struct Halves {
+    float c[4], s[4];
+
+    __device__ __forceinline__ void make(const QkvArgs& a, int pos)
+    {
+        const Turns turns(a, pos);
+        const bool high = threadIdx.x & 16;                // this lane's own pairs are 4 l + 2 and + 3
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float oc = __shfl_xor_sync(kAll, turns.c[k], 16), os = __shfl_xor_sync(kAll, turns.s[k], 16);
+            c[k] = high ? oc : turns.c[k];
+            s[k] = high ? os : turns.s[k];
+            c[2 + k] = high ? turns.c[k] : oc;
+            s[2 + k] = high ? turns.s[k] : os;
+        }
+    }
+    __device__ __forceinline__ void apply(const QkvArgs&, float (&x)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = x[i], v = x[i + 4];
+            x[i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(v, s[i]));
+            x[i + 4] = __fadd_rn(__fmul_rn(v, c[i]), __fmul_rn(u, s[i]));
+        }
+    }
+};
+struct NoTurn {
+    __device__ __forceinline__ void make(const QkvArgs&, int) {}
+    __device__ __forceinline__ void apply(const QkvArgs&, float (&)[8]) const {}
+};
 
 enum { kQuery = 0, kKey = 1, kValue = 2 };
 
 // A warp: heads [h0, h1) of one token's queries, keys or values, two at a
-// time (16 lanes a row), with kAhead loads under way: 24 warps an SM times 3
-// times 512 bytes cover the latency of the memory, which one load a warp did
-// not (16384 tokens of 32 + 16 heads: 97 us).
+// time (16 lanes a row), kAhead loads under way: where 8 rows are a warp's,
+// all of them are before the token's angles are made.
 // Rows that are not quantised are held split, where a pair (i, i + 64) is one
 // lane's; a group of a quantised row lies in few lanes only if they are whole.
-template <bool BF16, int KIND, int GROUP>
-__device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos, int h0, int h1, const Turns& turns)
+template <bool BF16, int KIND, int GROUP, bool NORM, class Turn>
+__device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos, int h0, int h1)
 {
     constexpr bool SPLIT = GROUP == 0;
-    constexpr int ESZ = BF16 ? 2 : 4;
+    constexpr int ESZ = BF16 ? 2 : 4, kAhead = GROUP ? 1 : 4;
     using R = Raw<BF16, SPLIT>;
     const int lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
     const RowSource& src = KIND == kQuery ? a.q : KIND == kKey ? a.k : a.v;
-    const void* weight = KIND == kQuery ? a.q_weight : KIND == kKey ? a.k_weight : nullptr;
     const char* from = static_cast<const char*>(src.data) + (b * src.batch + t * src.token + (h0 + half) * src.head + R::at(l)) * ESZ;
     const int64_t step = 2 * src.head * ESZ;
-    constexpr int kAhead = GROUP ? 1 : BF16 ? 3 : 2;
-    R next[kAhead];
+    // where the row goes: q_out, or the cache's row of this position
+    char* to = static_cast<char*>(KIND == kQuery ? a.q_out : KIND == kKey ? a.K : a.V);
+    const bool plain = to != nullptr;
+    const int64_t to_step = 2 * (KIND == kQuery ? a.q_out_head : (int64_t)a.n_max * kD) * ESZ;
+    const int64_t unit0 = (int64_t)b * a.Hkv + h0 + half;
+    if (KIND == kQuery) to += (b * a.q_out_batch + t * a.q_out_token + (h0 + half) * a.q_out_head + R::at(l)) * ESZ;
+    else to += ((unit0 * a.n_max + pos) * kD + R::at(l)) * ESZ;
+    const Kv4& four = KIND == kKey ? a.K4 : a.V4;
+    int64_t row4 = unit0 * four.R + pos;
+    R next[kAhead], w;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
         if (h0 + half + 2 * i < h1) next[i].load(from, 0);
         from += step;
     }
-    // where the row goes: q_out, or the cache's row of this position
-    const int64_t unit0 = (int64_t)b * a.Hkv + h0 + half;
-    char* to = static_cast<char*>(KIND == kQuery ? a.q_out : KIND == kKey ? a.K : a.V);
-    const bool plain = to != nullptr;
-    const int64_t to_step = 2 * (KIND == kQuery ? a.q_out_head : (int64_t)a.n_max * kD) * ESZ;
-    if (KIND == kQuery) to += (b * a.q_out_batch + t * a.q_out_token + (h0 + half) * a.q_out_head + R::at(l)) * ESZ;
-    else to += ((unit0 * a.n_max + pos) * kD + R::at(l)) * ESZ;
-    const Kv4& four = KIND == kKey ? a.K4 : a.V4;
-    int64_t row4 = unit0 * four.R + pos;
-    const float eps = a.eps;
-    const int rot = a.rot;
-    float f[8];
-    Rotation<SPLIT> turn;
-    if (KIND != kValue) {
-        if (weight) {
-            R w;
-            w.load(weight, R::at(l));
-            w.floats(f);
-        }
-        if (rot) turn.make(a, turns);
-    }
+    if (NORM) w.load(KIND == kQuery ? a.q_weight : a.k_weight, R::at(l));
+    Turn turn;
+    turn.make(a, pos);
     for (int left = h1 - h0; left > 0;) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (left <= 0) break;
             R raw = next[i];
-            const bool live = half < left;
             if (half + 2 * kAhead < left) next[i].load(from, 0);
             from += step;
+            const bool live = half < left;
             float x[8];
             if (KIND != kValue || GROUP) raw.floats(x);
             if (KIND != kValue) {
-                if (weight) {
-                    const float r = rsqrtf(fmaf(sum_squares<SPLIT>(x), 1.f / kD, eps));
+                if (NORM) {
+                    const float r = rsqrtf(fmaf(sum_squares<SPLIT>(x), 1.f / kD, a.eps));
+                    float f[8];
+                    w.floats(f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = x[e] * r * f[e];
                 }
-                if (rot) turn.apply(a, x);
+                turn.apply(a, x);
                 raw.set(x);
             }
             if (plain) {
@@ -490,9 +521,34 @@ __device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos,
     }
 }
 
+// queries or keys: with or without a norm, and by the kind of rotation
+template <bool BF16, int KIND, int GROUP>
+__device__ __forceinline__ void do_turned(const QkvArgs& a, int b, int t, int pos, int h0, int h1)
+{
+    const bool norm = (KIND == kQuery ? a.q_weight : a.k_weight) != nullptr;
+    if constexpr (GROUP == 0) {
+        if (a.rot == kD && !a.interleaved) {
+            if (norm) do_rows<BF16, KIND, GROUP, true, Halves>(a, b, t, pos, h0, h1);
+            else do_rows<BF16, KIND, GROUP, false, Halves>(a, b, t, pos, h0, h1);
+            return;
+        }
+    }
+    if (a.rot) {
+        if (norm) do_rows<BF16, KIND, GROUP, true, Rotation<GROUP == 0>>(a, b, t, pos, h0, h1);
+        else do_rows<BF16, KIND, GROUP, false, Rotation<GROUP == 0>>(a, b, t, pos, h0, h1);
+    } else {
+        if (norm) do_rows<BF16, KIND, GROUP, true, NoTurn>(a, b, t, pos, h0, h1);
+        else do_rows<BF16, KIND, GROUP, false, NoTurn>(a, b, t, pos, h0, h1);
+    }
+}
+
 // One warp: rows [r0, r1) of one token, q heads, then k heads, then v heads.
+// Few rows to a warp: what the machine works on at once then lies within some
+// megabytes of each tensor, which the memory needs for its bandwidth (without
+// norm and rotation, 16384 tokens of 32 + 16 heads: 84 us with a token to a
+// warp, whatever the depth of its loads).
 template <bool BF16, int GROUP>
-__global__ void __launch_bounds__(32 * kQkvWarps, 6) k_qkv(const __grid_constant__ QkvArgs a, int per_warp, int slices)
+__global__ void __launch_bounds__(32 * kQkvWarps, GROUP || BF16 ? 8 : 6) k_qkv(const __grid_constant__ QkvArgs a, int per_warp, int slices)
 {
     const int64_t w = (int64_t)blockIdx.x * kQkvWarps + (threadIdx.x >> 5);
     const int token = (int)(w / slices);
@@ -502,10 +558,9 @@ __global__ void __launch_bounds__(32 * kQkvWarps, 6) k_qkv(const __grid_constant
     if (pos < 0 || pos >= a.n_max) return;             // padding: nothing of this token is written
     const int nq = a.q.data ? a.Hq : 0, nk = nq + a.Hkv, rows = nk + a.Hkv;
     const int r0 = (int)(w - (int64_t)token * slices) * per_warp, r1 = min(r0 + per_warp, rows);
-    const Turns turns(a, r0 < nk ? pos : 0);
-    if (r0 < nq) do_rows<BF16, kQuery, 0>(a, b, t, pos, r0, min(r1, nq), turns);
-    if (r0 < nk && r1 > nq) do_rows<BF16, kKey, GROUP>(a, b, t, pos, max(r0, nq) - nq, min(r1, nk) - nq, turns);
-    if (r1 > nk) do_rows<BF16, kValue, GROUP>(a, b, t, pos, max(r0, nk) - nk, r1 - nk, turns);
+    if (r0 < nq) do_turned<BF16, kQuery, 0>(a, b, t, pos, r0, min(r1, nq));
+    if (r0 < nk && r1 > nq) do_turned<BF16, kKey, GROUP>(a, b, t, pos, max(r0, nq) - nq, min(r1, nk) - nq);
+    if (r1 > nk) do_rows<BF16, kValue, GROUP, false, NoTurn>(a, b, t, pos, max(r0, nk) - nk, r1 - nk);
 }
 
 // 16 lanes a row: its K, its V, or both
@@ -538,7 +593,17 @@ cudaError_t launch_qkv_t(const QkvArgs& a, int sms, cudaStream_t st)
 {
     const int rows = (a.q.data ? a.Hq : 0) + 2 * a.Hkv;
     const int64_t tokens = (int64_t)a.B * a.T;
-    const int per_warp = tokens * rows <= (int64_t)sms * 64 ? 2 : rows;
+    // Few rows: two to a warp, spread over the machine.  Many: eight, which
+    // share the work on the token's angles; rows to quantise are bound by
+    // their arithmetic, so as many of a token as leave 32 warps to an SM
+    // (16384 tokens of 32 + 16 heads: 101 us, eight to a warp 140 us; 2000
+    // tokens: a whole token to a warp 20.7 us).
+    const int64_t all = tokens * rows;
+    int per_warp = all <= (int64_t)sms * 128 ? 2 : 8;
+    if (a.group && per_warp == 8) {
+        const int64_t fair = all / ((int64_t)sms * 32) / 2 * 2;
+        per_warp = fair < 8 ? 8 : fair < rows ? (int)fair : rows;
+    }
     const int slices = (rows + per_warp - 1) / per_warp;
     const int64_t grid = (tokens * slices + kQkvWarps - 1) / kQkvWarps;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
