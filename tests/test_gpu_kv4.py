@@ -514,6 +514,104 @@ def test_offsets_beyond_32_bits():
     assert off <= 2.0 ** -11, off
 
 
+def test_long_sequences_of_a_full_machine():
+    """32 units of 131072 rows: 100 tiles to a warp, where sums that lose a little with every step show it.  The bound is that of
+    the short sequences: sums are rounded to nearest, so their errors do not add up in one direction."""
+    B, H, n, group = 4, 8, 131072, 32
+    cfg = config(B, 4 * H, H, n, torch.bfloat16)
+    buf = [torch.zeros(ckv.ckv_kv4_bytes(cfg, group), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for first in range(0, n, n // 4):
+        pos = (torch.arange(n // 4, dtype=torch.int32, device="cuda") + first).repeat(B, 1)
+        k, v = (torch.randn((B, n // 4, H, D), generator=gen, device="cuda").bfloat16() for _ in range(2))
+        ckv.ckv_kv4_write(cfg, group, k, v, pos, *buf)
+    del k, v
+    q = (1.5 * torch.randn((B, 4 * H, D), generator=gen, device="cuda")).bfloat16()
+    out = torch.empty((B, 4 * H, D), device="cuda")
+    lse = torch.empty((B, 4 * H), device="cuda")
+    work = torch.zeros(ckv.ckv_kv4_workspace(cfg), dtype=torch.uint8, device="cuda")
+    ckv.ckv_kv4_dense_decode(cfg, group, q, *buf, n, None, work, out, lse)
+    for unit in (0, 19, 31):
+        rows = []
+        for i, b in enumerate(buf):
+            at, cut = unit * n * 64, B * H * n * 64
+            one = torch.cat([b[at:at + n * 64], b[cut + unit * n * 16:cut + (unit + 1) * n * 16]])
+            rows.append(torch.from_numpy(ref.values_of(one, 1, 1, n, group, bool(i))[0, 0]).cuda())
+        b, h = divmod(unit, H)
+        z = q[b, 4 * h:4 * h + 4].double() @ rows[0].T / D ** 0.5
+        want = torch.softmax(z, -1) @ rows[1]
+        err = (out[b, 4 * h:4 * h + 4].double() - want).norm(dim=-1) / want.norm(dim=-1)
+        assert float(err.max()) <= 3e-6 + 4 * U32 * float(z.abs().max()), (unit, err)
+        assert float((lse[b, 4 * h:4 * h + 4].double() - torch.logsumexp(z, -1)).abs().max()) <= 2e-5
+
+
+def test_more_units_than_threads_of_a_block():
+    rng = np.random.default_rng(31)
+    B, Hkv = 40, 8
+    lens = rng.integers(0, 70, B).tolist()
+    Case(rng, B, 16, Hkv, 70, 69, 64, "bf16", lens=lens).run().check()
+    rows = torch.from_numpy(rng.integers(0, 64, (6 * 64, 9)).astype(np.int32)).cuda()
+    n_rows = torch.from_numpy(rng.integers(0, 10, 6 * 64).astype(np.int32)).cuda()
+    Case(rng, 6, 64, 8, 64, 60, 32, "f32", sinks=3, rows=rows, n_rows=n_rows, max_rows=9, per_head=True,
+         lens=[60, 1, 0, 33, 4, 3]).run().check()
+
+
+def test_no_listed_rows():
+    rng = np.random.default_rng(32)
+    c = Case(rng, 2, 4, 2, 30, 20, 32, "bf16", sinks=4, rows=torch.empty((4, 0), dtype=torch.int32, device="cuda"),
+             n_rows=torch.tensor([5, 0, -1, 0], dtype=torch.int32, device="cuda"), max_rows=0)
+    c.run().check()
+    first = c.out.clone()
+    ckv.ckv_kv4_attend_rows(c.cfg, c.group, c.q, c.K4, c.V4, c.n, None, None, c.n_rows, 0, c.work, c.out)
+    assert torch.equal(c.out, first)
+
+
+def test_a_cache_as_the_source_of_rows():
+    # [B][H][n_max][D] caches into 4 bits at rows 0 .. T-1, and many heads
+    B, H, n, group = 2, 65, 33, 64
+    cfg = config(B, 2 * H, H, n, torch.bfloat16)
+    K, V = (torch.randn((B, H, n, D), device="cuda").bfloat16() for _ in range(2))
+    buf = [torch.zeros(ckv.ckv_kv4_bytes(cfg, group), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ckv.ckv_kv4_write(cfg, group, K.transpose(1, 2)[:, :20], V.transpose(1, 2)[:, :20], None, *buf)
+    for i, t in enumerate((K, V)):
+        code, scale, middle = ref.quantise(f32(t[:, :, :20]), group)
+        want = (middle[..., None] + scale[..., None] * code.reshape(B, H, 20, D // group, group)).reshape(B, H, 20, D)
+        got = ref.values_of(buf[i], B, H, n, group, bool(i))
+        np.testing.assert_array_equal(got[:, :, :20], want)
+        assert not got[:, :, 20:].any()
+    # every head of a token through the norm and rotation as well
+    x = torch.randn((B, 3, 4 * H, D), device="cuda").bfloat16()
+    pos = torch.tensor([[5, -1, 32], [0, 1, 2]], dtype=torch.int32, device="cuda")
+    out = torch.zeros((B, 3, 2 * H, D), dtype=torch.bfloat16, device="cuda")
+    freq = 1.0e4 ** (-np.arange(0, D, 2) / D)
+    ckv.ckv_qk_norm_rope(cfg, x[:, :, :2 * H], x[:, :, 2 * H:3 * H], x[:, :, 3 * H:], pos, out, freq, K=K, V=V)
+    want, bound = ref.rotated(f64(x[:, :, :2 * H]), pos.cpu().numpy(), None, 0, freq, False, 1.0)
+    want[0, 1], bound[0, 1] = 0, 0
+    assert (np.abs(f64(out) - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound)).all()
+    assert torch.equal(V[1, :, :3], x[1, :, 3 * H:].transpose(0, 1)) and torch.equal(V[0, :, 32], x[0, 2, 3 * H:])
+
+
+def test_rotated_rows_equal_an_eager_norm_and_rotation():
+    # the fixed order of the sum of squares and one rounding a step: the same bits as elementary operations in 32 bits
+    B, T, H = 2, 300, 4
+    cfg = config(B, H, H, T, torch.float32)
+    x = torch.randn((B, T, 3 * H, D), device="cuda")
+    w = 1 + 0.1 * torch.randn(D, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda").repeat(B, 1)
+    freq = 1.0e6 ** (-np.arange(0, D, 2) / D)
+    out, K, V = torch.empty((B, T, H, D), device="cuda"), *(torch.empty((B, H, T, D), device="cuda") for _ in range(2))
+    ckv.ckv_qk_norm_rope(cfg, x[:, :, :H], x[:, :, H:2 * H], x[:, :, 2 * H:], pos, out, freq, q_weight=w, k_weight=w, K=K, V=V)
+    y = x[:, :, :H]
+    y = y * torch.rsqrt(y.square().mean(-1, keepdim=True) + 1e-6) * w
+    ang = (pos.double()[..., None] * torch.from_numpy(freq).cuda())[:, :, None]
+    c, s = ang.cos().float(), ang.sin().float()
+    a, b = y[..., :64], y[..., 64:]
+    want = torch.cat([a * c - b * s, b * c + a * s], -1)
+    # a cosine rounded next to a border may differ by one step of 2^-24: of 600 x 64 cosines, at 2^-49 off, none is expected
+    assert float((out != want).float().mean()) < 1e-4
+    assert float((out - want).abs().max()) <= 2.0 ** -22 * float(want.abs().max())
+
+
 # ------------------------------------------------------- as they are used
 def test_decode_steps_on_a_4_bit_cache():
     """A prompt's rows into both kinds of cache, then steps of one token: norm and rotation, the append, dense attention and
