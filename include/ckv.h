@@ -442,7 +442,8 @@ size_t ckv_kv4_bytes(const ckv_config* cfg, int group);   /* 0 for a bad argumen
  * nothing of it is read or written, its q_out row stays as it was.  Two tokens of one
  * sequence at the same position leave an unspecified mixture in that row.
  * Strides are in elements, for batch, token and head; channels are
- * contiguous; a multiple of 16 bytes each.  q_out may be q (in place).
+ * contiguous; a multiple of 16 bytes each (where there is more than one).
+ * q_out may be q (in place).
  * Errors: CKV_ERR_INVALID_ARG (also: K without V, K4 without V4, no cache at
  * all, an inv_freq that is not finite), CKV_ERR_CUDA. */
 typedef struct {

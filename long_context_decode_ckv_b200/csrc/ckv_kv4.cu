@@ -54,12 +54,14 @@ ckv_status status_of(cudaError_t e)
 
 int64_t kv_units(const ckv_config* c) { return (int64_t)c->batch * c->n_kv_heads; }
 
-// a row source: 16-byte loads need 16-byte rows
-bool valid_rows(const void* p, const int64_t* stride, int esz)
+// rows [batch][tokens][heads]: 16-byte loads need 16-byte rows; the stride of
+// a single one does not matter
+bool valid_rows(const void* p, const int64_t* stride, int batch, int tokens, int heads, int esz)
 {
+    const int size[3] = {batch, tokens, heads};
     if (!aligned(p, 16)) return false;
     for (int i = 0; i < 3; ++i)
-        if (stride[i] % (16 / esz)) return false;
+        if (size[i] > 1 && stride[i] % (16 / esz)) return false;
     return true;
 }
 
@@ -143,8 +145,9 @@ CKV_API ckv_status ckv_qk_norm_rope(const ckv_config* cfg, const ckv_qkv* x, voi
         return CKV_ERR_INVALID_ARG;
     if (!(x->eps >= 0.f) || isinf(x->eps) || !isfinite(x->rot_scale)) return CKV_ERR_INVALID_ARG;
     const int esz = cfg->kv_dtype == CKV_BF16 ? 2 : 4;
-    if (!valid_rows(x->q, x->q_stride, esz) || !valid_rows(x->k, x->k_stride, esz) ||
-        !valid_rows(x->v, x->v_stride, esz) || !valid_rows(x->q_out, x->q_out_stride, esz))
+    const int B = cfg->batch, T = x->n_tokens, Hq = cfg->n_q_heads, Hkv = cfg->n_kv_heads;
+    if (!valid_rows(x->q, x->q_stride, B, T, Hq, esz) || !valid_rows(x->k, x->k_stride, B, T, Hkv, esz) ||
+        !valid_rows(x->v, x->v_stride, B, T, Hkv, esz) || !valid_rows(x->q_out, x->q_out_stride, B, T, Hq, esz))
         return CKV_ERR_INVALID_ARG;
     if (!aligned(x->K, 16) || !aligned(x->V, 16) || !aligned(x->K4, 16) || !aligned(x->V4, 16) ||
         !aligned(x->q_weight, 16) || !aligned(x->k_weight, 16))
@@ -197,7 +200,8 @@ CKV_API ckv_status ckv_kv4_write(const ckv_config* cfg, int group, const void* k
     if (n_tokens < 0 || (int64_t)cfg->batch * n_tokens > INT32_MAX || (!pos && n_tokens > cfg->n_max))
         return CKV_ERR_INVALID_ARG;
     const int esz = cfg->kv_dtype == CKV_BF16 ? 2 : 4;
-    if (!valid_rows(k, k_stride_host, esz) || !valid_rows(v, v_stride_host, esz) || !aligned(K4, 16) || !aligned(V4, 16))
+    if (!valid_rows(k, k_stride_host, cfg->batch, n_tokens, cfg->n_kv_heads, esz) ||
+        !valid_rows(v, v_stride_host, cfg->batch, n_tokens, cfg->n_kv_heads, esz) || !aligned(K4, 16) || !aligned(V4, 16))
         return CKV_ERR_INVALID_ARG;
     if (n_tokens == 0) return CKV_OK;
     ckv::QkvArgs a{};

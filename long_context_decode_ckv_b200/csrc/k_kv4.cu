@@ -347,9 +347,9 @@ struct Warp {
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             const uint32_t most = __reduce_max_sync(kFull, __float_as_uint(sc[j]));
-            // scale < 2^e
+            // scale < 2^e; the format's scales are below 2^126
             int e = (int)((most >> 23) & 255u) - 126;
-            e = e < -99 ? -99 : e;
+            e = e < -99 ? -99 : e > 126 ? 126 : e;
             const float now = fminf(c[j], __uint_as_float((uint32_t)(127 + 1 - e) << 23)), f = now / c[j];
             c[j] = now;
 #pragma unroll
@@ -461,6 +461,13 @@ struct Warp {
                 }
             }
         }
+        // ---- values: A is 16 channels x 16 rows
+        Words<2> v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = rows[e], chunk = (g >> 1) ^ ((r >> 1) & 2);
+            v[e] = lds<2>(st + S::V + r * kRowCodes + 16 * chunk + 8 * (g & 1));
+        }
         bool more = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -538,13 +545,7 @@ struct Warp {
                         pb[nt][j][k] = fma2(wd[nt][k], vs.w[j], fma2(wb[nt][k], vs.w[j], mul2(wa[nt][k], vs.w[j])));
             }
         }
-        // ---- values: A is 16 channels x 16 rows
-        Words<2> v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = rows[e], chunk = (g >> 1) ^ ((r >> 1) & 2);
-            v[e] = lds<2>(st + S::V + r * kRowCodes + 16 * chunk + 8 * (g & 1));
-        }
+        // A is 16 channels x 16 rows
 #pragma unroll
         for (int J = 0; J < 4; ++J) {
             const uint32_t sel = J & 1 ? 0x7632u : 0x5410u;

@@ -91,6 +91,11 @@ def test_norm_rope_arguments_checked(L):
     for name in ("q_stride", "k_stride", "v_stride", "q_out_stride"):
         for stride in ((4, 1024, 128), (4096, 1025, 128), (4096, 1024, 132)):
             assert call(c, qkv(**{name: (ctypes.c_int64 * 3)(*stride)})) == BAD
+    # the stride of a single batch, token or head does not matter (the call goes on to look for its device)
+    one = config(batch=1, n_q_heads=1, n_kv_heads=1, device=63)
+    odd = {name: (ctypes.c_int64 * 3)(5, 7, 9) for name in ("q_stride", "k_stride", "v_stride", "q_out_stride")}
+    assert call(one, qkv(n_tokens=0, **odd)) == ckv.CKV_OK
+    assert call(one, qkv(n_tokens=0, **{**odd, "q": ODD})) == BAD
     f = (ctypes.c_double * 64)(*([1.0] * 63 + [float("inf")]))
     assert call(c, qkv(inv_freq_host=ctypes.cast(f, ctypes.c_void_p))) == BAD
     assert call(c, qkv(n_tokens=0)) == ckv.CKV_OK                       # nothing to do, nothing launched
