@@ -15,7 +15,7 @@
 // 16 lanes hold one row, 8 channels each; a warp holds two rows at a time and
 // walks its share of one token's rows.  Memory bound where nothing is
 // quantised: (Hq + 2 Hkv) rows read and written once per token (16384 tokens
-// of 32 + 16 heads, 403 MB: 86 us, 4.7 TB/s; without norm and rotation 74 us,
+// of 32 + 16 heads, 403 MB: 82 us, 4.9 TB/s; without norm and rotation 70 us,
 // a plain copy of as much 62 us).  Quantised rows are bound by instructions,
 // about 200 for two rows (16384 x 16 rows to groups of 32: 36 us, 2.5 TB/s).
 #include <cuda_bf16.h>
@@ -29,7 +29,7 @@ namespace ckv {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kQkvWarps = 4;
+constexpr int kQkvWarps = 4;                   // at least 2: 64 threads fetch the frequencies
 
 // Quantisation of the group that holds this lane's 8 channels: the 16 lanes
 // of a row call together; group / 8 neighbouring lanes share a group.
@@ -304,7 +304,9 @@ __device__ __forceinline__ void turn_by(double t, float& c, float& s)
 // those of pairs 4 l + 2 half and + 1.
 struct Turns {
     float c[2], s[2];
-    __device__ __forceinline__ Turns(const QkvArgs& a, int pos)
+    // freq: the frequencies in shared memory (read by lane from the kernel's
+    // arguments, they would come one lane at a time)
+    __device__ __forceinline__ Turns(const QkvArgs& a, const double* freq, int pos)
     {
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -313,7 +315,7 @@ struct Turns {
             c[k] = 1.f;
             s[k] = 0.f;
             if (i < a.rot / 2) {
-                turn_by((double)pos * a.turn[i], c[k], s[k]);
+                turn_by((double)pos * freq[i], c[k], s[k]);
                 c[k] *= a.rot_scale;
                 s[k] *= a.rot_scale;
             }
@@ -369,9 +371,9 @@ struct Rotation {
     float c[8], s[8];        // interleaved: of the lane's 4 pairs, in [0, 4)
 
     static __device__ __forceinline__ int channel(int l, int e) { return SPLIT ? (e < 4 ? 4 * l + e : 60 + 4 * l + e) : 8 * l + e; }
-    __device__ __forceinline__ void make(const QkvArgs& a, int pos)
+    __device__ __forceinline__ void make(const QkvArgs& a, const double* freq, int pos)
     {
-        const Turns turns(a, pos);
+        const Turns turns(a, freq, pos);
         const int l = threadIdx.x & 15, half = a.rot / 2;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -419,9 +421,9 @@ struct Rotation {
 struct Halves {
     float c[4], s[4];
 
-    __device__ __forceinline__ void make(const QkvArgs& a, int pos)
+    __device__ __forceinline__ void make(const QkvArgs& a, const double* freq, int pos)
     {
-        const Turns turns(a, pos);
+        const Turns turns(a, freq, pos);
         const bool high = threadIdx.x & 16;                // this lane's own pairs are 4 l + 2 and + 3
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -443,19 +445,19 @@ struct Halves {
     }
 };
 struct NoTurn {
-    __device__ __forceinline__ void make(const QkvArgs&, int) {}
+    __device__ __forceinline__ void make(const QkvArgs&, const double*, int) {}
     __device__ __forceinline__ void apply(const QkvArgs&, float (&)[8]) const {}
 };
 
 enum { kQuery = 0, kKey = 1, kValue = 2 };
 
 // A warp: heads [h0, h1) of one token's queries, keys or values, two at a
-// time (16 lanes a row), kAhead loads under way: where 8 rows are a warp's,
-// all of them are before the token's angles are made.
+// time (16 lanes a row), kAhead loads under way: where no warp has more than
+// 8 rows (not LONG), all of them are before the token's angles are made.
 // Rows that are not quantised are held split, where a pair (i, i + 64) is one
 // lane's; a group of a quantised row lies in few lanes only if they are whole.
-template <bool BF16, int KIND, int GROUP, bool NORM, class Turn>
-__device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos, int h0, int h1)
+template <bool BF16, int KIND, int GROUP, bool LONG, bool NORM, class Turn>
+__device__ __forceinline__ void do_rows(const QkvArgs& a, const double* freq, int b, int t, int pos, int h0, int h1)
 {
     constexpr bool SPLIT = GROUP == 0;
     constexpr int ESZ = BF16 ? 2 : 4, kAhead = GROUP ? 1 : 4;
@@ -481,14 +483,16 @@ __device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos,
     }
     if (NORM) w.load(KIND == kQuery ? a.q_weight : a.k_weight, R::at(l));
     Turn turn;
-    turn.make(a, pos);
+    turn.make(a, freq, pos);
     for (int left = h1 - h0; left > 0;) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (left <= 0) break;
             R raw = next[i];
-            if (half + 2 * kAhead < left) next[i].load(from, 0);
-            from += step;
+            if (LONG) {
+                if (half + 2 * kAhead < left) next[i].load(from, 0);
+                from += step;
+            }
             const bool live = half < left;
             float x[8];
             if (KIND != kValue || GROUP) raw.floats(x);
@@ -518,27 +522,28 @@ __device__ __forceinline__ void do_rows(const QkvArgs& a, int b, int t, int pos,
             }
             left -= 2;
         }
+        if (!LONG) break;
     }
 }
 
 // queries or keys: with or without a norm, and by the kind of rotation
-template <bool BF16, int KIND, int GROUP>
-__device__ __forceinline__ void do_turned(const QkvArgs& a, int b, int t, int pos, int h0, int h1)
+template <bool BF16, int KIND, int GROUP, bool LONG>
+__device__ __forceinline__ void do_turned(const QkvArgs& a, const double* freq, int b, int t, int pos, int h0, int h1)
 {
     const bool norm = (KIND == kQuery ? a.q_weight : a.k_weight) != nullptr;
     if constexpr (GROUP == 0) {
         if (a.rot == kD && !a.interleaved) {
-            if (norm) do_rows<BF16, KIND, GROUP, true, Halves>(a, b, t, pos, h0, h1);
-            else do_rows<BF16, KIND, GROUP, false, Halves>(a, b, t, pos, h0, h1);
+            if (norm) do_rows<BF16, KIND, GROUP, LONG, true, Halves>(a, freq, b, t, pos, h0, h1);
+            else do_rows<BF16, KIND, GROUP, LONG, false, Halves>(a, freq, b, t, pos, h0, h1);
             return;
         }
     }
     if (a.rot) {
-        if (norm) do_rows<BF16, KIND, GROUP, true, Rotation<GROUP == 0>>(a, b, t, pos, h0, h1);
-        else do_rows<BF16, KIND, GROUP, false, Rotation<GROUP == 0>>(a, b, t, pos, h0, h1);
+        if (norm) do_rows<BF16, KIND, GROUP, LONG, true, Rotation<GROUP == 0>>(a, freq, b, t, pos, h0, h1);
+        else do_rows<BF16, KIND, GROUP, LONG, false, Rotation<GROUP == 0>>(a, freq, b, t, pos, h0, h1);
     } else {
-        if (norm) do_rows<BF16, KIND, GROUP, true, NoTurn>(a, b, t, pos, h0, h1);
-        else do_rows<BF16, KIND, GROUP, false, NoTurn>(a, b, t, pos, h0, h1);
+        if (norm) do_rows<BF16, KIND, GROUP, LONG, true, NoTurn>(a, freq, b, t, pos, h0, h1);
+        else do_rows<BF16, KIND, GROUP, LONG, false, NoTurn>(a, freq, b, t, pos, h0, h1);
     }
 }
 
@@ -550,6 +555,10 @@ __device__ __forceinline__ void do_turned(const QkvArgs& a, int b, int t, int po
 template <bool BF16, int GROUP>
 __global__ void __launch_bounds__(32 * kQkvWarps, GROUP || BF16 ? 8 : 6) k_qkv(const __grid_constant__ QkvArgs a, int per_warp, int slices)
 {
+    constexpr bool LONG = GROUP != 0;
+    __shared__ double freq[kD / 2];
+    if (threadIdx.x < a.rot / 2) freq[threadIdx.x] = a.turn[threadIdx.x];
+    if (a.rot) __syncthreads();
     const int64_t w = (int64_t)blockIdx.x * kQkvWarps + (threadIdx.x >> 5);
     const int token = (int)(w / slices);
     if (token >= a.B * a.T) return;
@@ -558,9 +567,9 @@ __global__ void __launch_bounds__(32 * kQkvWarps, GROUP || BF16 ? 8 : 6) k_qkv(c
     if (pos < 0 || pos >= a.n_max) return;             // padding: nothing of this token is written
     const int nq = a.q.data ? a.Hq : 0, nk = nq + a.Hkv, rows = nk + a.Hkv;
     const int r0 = (int)(w - (int64_t)token * slices) * per_warp, r1 = min(r0 + per_warp, rows);
-    if (r0 < nq) do_turned<BF16, kQuery, 0>(a, b, t, pos, r0, min(r1, nq));
-    if (r0 < nk && r1 > nq) do_turned<BF16, kKey, GROUP>(a, b, t, pos, max(r0, nq) - nq, min(r1, nk) - nq);
-    if (r1 > nk) do_rows<BF16, kValue, GROUP, false, NoTurn>(a, b, t, pos, max(r0, nk) - nk, r1 - nk);
+    if (r0 < nq) do_turned<BF16, kQuery, 0, LONG>(a, freq, b, t, pos, r0, min(r1, nq));
+    if (r0 < nk && r1 > nq) do_turned<BF16, kKey, GROUP, LONG>(a, freq, b, t, pos, max(r0, nq) - nq, min(r1, nk) - nq);
+    if (r1 > nk) do_rows<BF16, kValue, GROUP, LONG, false, NoTurn>(a, freq, b, t, pos, max(r0, nk) - nk, r1 - nk);
 }
 
 // 16 lanes a row: its K, its V, or both
