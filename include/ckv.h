@@ -408,7 +408,7 @@ ckv_status ckv_attend_rows_static(const ckv_config* cfg, const void* q, const vo
  * of the rows and of 16/32-bit caches) and device, and what else a call
  * names.  They run on cfg->device whatever device is current (restored on
  * return), only enqueue work on `stream`, allocate nothing and can be
- * captured into a graph.  n_max may be at most 2^31 - 65, batch * n_q_heads at
+ * captured into a graph.  n_max may be at most 2^31 - 1024, batch * n_q_heads at
  * most 2^20; pointers are 16-byte aligned.
  *
  * The 4-bit cache of K (or of V) is one buffer of ckv_kv4_bytes(cfg, group)

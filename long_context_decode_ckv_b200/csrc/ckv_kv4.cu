@@ -21,7 +21,7 @@ constexpr int kMaxDevices = 64;
 bool valid_shape(const ckv_config* c)
 {
     if (!c || c->batch < 1 || c->n_q_heads < 1 || c->n_kv_heads < 1 || c->n_q_heads % c->n_kv_heads) return false;
-    if (c->head_dim != ckv::kD || c->n_max < 1 || c->n_max > INT32_MAX - 64) return false;
+    if (c->head_dim != ckv::kD || c->n_max < 1 || c->n_max > INT32_MAX - 1023) return false;
     if (c->kv_dtype != CKV_F32 && c->kv_dtype != CKV_BF16) return false;
     if ((int64_t)c->batch * c->n_q_heads > (1 << 20)) return false;
     return c->device >= 0 && c->device < kMaxDevices;
@@ -83,7 +83,7 @@ ckv_status attend(const ckv_config* cfg, int group, const void* q, const void* K
     const bool per_head = listed && cfg->mode == CKV_PER_HEAD;
     if (listed) {
         if (cfg->mode != CKV_PER_HEAD && cfg->mode != CKV_QUERY_GROUP) return CKV_ERR_INVALID_ARG;
-        if (cfg->n_sinks < 0 || max_rows < 0 || (int64_t)cfg->n_sinks + max_rows > INT32_MAX - 64) return CKV_ERR_INVALID_ARG;
+        if (cfg->n_sinks < 0 || max_rows < 0 || (int64_t)cfg->n_sinks + max_rows > INT32_MAX - 1023) return CKV_ERR_INVALID_ARG;
         if (!n_rows || (max_rows > 0 && !rows)) return CKV_ERR_INVALID_ARG;
     }
     const int NH = per_head ? 1 : Gq;

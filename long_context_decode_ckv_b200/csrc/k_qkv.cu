@@ -572,28 +572,37 @@ __global__ void __launch_bounds__(32 * kQkvWarps, GROUP || BF16 ? 8 : 6) k_qkv(c
     if (r1 > nk) do_rows<BF16, kValue, GROUP, LONG, false, NoTurn>(a, freq, b, t, pos, max(r0, nk) - nk, r1 - nk);
 }
 
-// 16 lanes a row: its K, its V, or both
+// 16 lanes a row, kReadRows rows 16 apart for each lane: their K, their V, or
+// both, all loaded before the first is stored
+constexpr int kReadRows = 2;
 template <bool BF16, int GROUP>
 __global__ void __launch_bounds__(256) k_kv4_read(const __grid_constant__ Kv4ReadArgs a)
 {
     const int l = threadIdx.x & 15;
-    const int i = blockIdx.x * 16 + (threadIdx.x >> 4);    // row of the unit's range
-    if (i >= a.count) return;
+    const int i0 = blockIdx.x * (16 * kReadRows) + (threadIdx.x >> 4);   // row of the unit's range
     const int64_t unit = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
     if (unit >= a.units) return;
-    const int64_t row = a.first + i;
-    float x[8], y[8];
-    Raw<BF16, false> raw;
-    if (a.K) kv4_load<GROUP, false>(a.K4, unit * a.K4.R + row, l, x);
-    if (a.V) kv4_load<GROUP, true>(a.V4, unit * a.V4.R + row, l, y);
-    const int64_t to = (unit * a.n_max + row) * kD + 8 * l;
-    if (a.K) {
-        raw.set(x);
-        raw.store(a.K, to);
+    const int64_t row0 = a.first + i0;
+    float x[kReadRows][8], y[kReadRows][8];
+#pragma unroll
+    for (int k = 0; k < kReadRows; ++k) {
+        if (i0 + 16 * k >= a.count) break;
+        if (a.K) kv4_load<GROUP, false>(a.K4, unit * a.K4.R + row0 + 16 * k, l, x[k]);
+        if (a.V) kv4_load<GROUP, true>(a.V4, unit * a.V4.R + row0 + 16 * k, l, y[k]);
     }
-    if (a.V) {
-        raw.set(y);
-        raw.store(a.V, to);
+    const int64_t to = (unit * a.n_max + row0) * kD + 8 * l;
+    Raw<BF16, false> raw;
+#pragma unroll
+    for (int k = 0; k < kReadRows; ++k) {
+        if (i0 + 16 * k >= a.count) break;
+        if (a.K) {
+            raw.set(x[k]);
+            raw.store(a.K, to + 16 * k * kD);
+        }
+        if (a.V) {
+            raw.set(y[k]);
+            raw.store(a.V, to + 16 * k * kD);
+        }
     }
 }
 
@@ -625,7 +634,7 @@ template <bool BF16>
 cudaError_t launch_read_t(const Kv4ReadArgs& a, cudaStream_t st)
 {
     const int64_t y = a.units < 32768 ? a.units : 32768, z = (a.units + y - 1) / y;
-    const dim3 grid((unsigned)((a.count + 15) / 16), (unsigned)y, (unsigned)z);
+    const dim3 grid((unsigned)((a.count - 1) / (16 * kReadRows) + 1), (unsigned)y, (unsigned)z);
     auto fn = a.group == 32 ? k_kv4_read<BF16, 32> : a.group == 64 ? k_kv4_read<BF16, 64> : k_kv4_read<BF16, 128>;
     fn<<<grid, 256, 0, st>>>(a);
     return cudaGetLastError();
