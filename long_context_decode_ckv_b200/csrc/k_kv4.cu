@@ -934,15 +934,18 @@ cudaError_t launch_attend_t(const Kv4AttendArgs& a, int bf16, int sms, cudaStrea
     const long long tiles = ROWS ? ((long long)a.S + a.max_rows + 1 + kTile - 1) / kTile : (a.n + kTile - 1) / kTile;
     const long long most = kCtasPerSM<NT> * sms < kKv4MaxCtas ? kCtasPerSM<NT> * sms : kKv4MaxCtas;
     // Few tiles: shares that start and end with units (where all are as long
-    // as the longest), a CTA for each unit while a warp has up to 3 tiles; a
-    // merge through slots costs about as much as two more tiles.  Many
-    // tiles: the whole machine, wherever the shares' borders fall.
+    // as the longest), a CTA for each unit while a warp has up to 3 tiles (a
+    // merge through slots costs about as much as two more: 32 tiles a unit of
+    // 8, 10.7 us, with one CTA each 12.8), and one CTA to an SM (32 units of
+    // 47 tiles 12.2 us, with more 13.9; 128 lists of 33 tiles 20.0 and 22.8, 32
+    // lists of 129 tiles 23.4 and 22.7).  Many tiles: the whole machine,
+    // wherever the shares' borders fall.
     long long P = (long long)a.U * tiles;
     if (P > most * kWarps * 4) P = most;
     else {
         const long long each = tiles <= 3 * kWarps ? 1 : (tiles + kWarps - 1) / kWarps;
         P = a.U * each;
-        if (P > most) P = a.U < most ? most / a.U * a.U : most;
+        if (P > sms) P = a.U < sms ? sms / a.U * a.U : most;
     }
     fn<<<(unsigned)P, kThreads, kWarps * kWarpSmem<NG>, st>>>(a, bf16);
     return cudaGetLastError();
