@@ -484,7 +484,8 @@ ckv_status ckv_kv4_read(const ckv_config* cfg, int group, const void* K4, const 
                         void* K, void* V, void* stream);
 
 /* Scratch of the two calls below: bytes of device memory, cleared to zero
- * once before its first use and left ready for the next call by each call.
+ * once before its first use and left ready for the next call by each call,
+ * whatever that one's configuration: a buffer of the largest size serves all.
  * Calls that may run at the same time (two streams, two graphs replayed at
  * once) need a workspace each. */
 size_t ckv_kv4_workspace(const ckv_config* cfg);           /* 0 for a bad argument */

@@ -65,10 +65,11 @@ bool valid_rows(const void* p, const int64_t* stride, int batch, int tokens, int
     return true;
 }
 
-size_t workspace_counters(const ckv_config* c)
-{
-    return ((size_t)c->batch * c->n_q_heads * sizeof(unsigned) + 255) / 256 * 256;
-}
+// The counters at the head of a workspace, as many for every configuration:
+// where they end may not depend on the call, since one call's partial results
+// would lie where the next one, of another batch, expects zeros.
+constexpr size_t kCounterBytes = ckv::kKv4MaxCtas * sizeof(unsigned);
+static_assert(kCounterBytes % 256 == 0, "aligned partial results");
 
 // everything of an attention call but its row lists
 ckv_status attend(const ckv_config* cfg, int group, const void* q, const void* K4, const void* V4, int n,
@@ -113,7 +114,7 @@ ckv_status attend(const ckv_config* cfg, int group, const void* q, const void* K
         a.S = cfg->n_sinks;
     }
     a.cnt = static_cast<unsigned*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + workspace_counters(cfg));
+    a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterBytes);
     a.out = out;
     a.lse = lse;
     return status_of(ckv::launch_kv4_attend(a, cfg->kv_dtype == CKV_BF16, sms, (cudaStream_t)stream));
@@ -131,7 +132,7 @@ CKV_API size_t ckv_kv4_workspace(const ckv_config* cfg)
 {
     if (!valid_shape(cfg)) return 0;
     const size_t Hq = cfg->n_q_heads, NH = Hq / cfg->n_kv_heads;
-    return workspace_counters(cfg) + (cfg->batch * Hq + ckv::kKv4MaxCtas * NH) * (2 + ckv::kD) * sizeof(float);
+    return kCounterBytes + (cfg->batch * Hq + ckv::kKv4MaxCtas * NH) * (2 + ckv::kD) * sizeof(float);
 }
 
 CKV_API ckv_status ckv_qk_norm_rope(const ckv_config* cfg, const ckv_qkv* x, void* stream)

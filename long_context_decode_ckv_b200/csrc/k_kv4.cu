@@ -899,19 +899,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
                 so[i] = merge_warps<NG>(red, kRedWarp, i / kD, i % kD, M, L);
                 if (i % kD == 0) sm[i / kD] = make_float2(M, L);
             }
-            // ---- arrival; the unit's last piece merges every slot.  The
-            // barrier orders the CTA's stores before thread 0's fence, which
+            // ---- arrival; the unit's last piece merges every slot.  A unit of
+            // several pieces is the last one of its first CTA's share, so that
+            // CTA's counter is this unit's alone.  The barrier orders the CTA's stores before thread 0's fence, which
             // makes them visible before its arrival; likewise the other way.
             __syncthreads();
             if (tid == 0) {
                 __threadfence();
-                s_last = atomicAdd(a.cnt + u, 1u) == (unsigned)(pl - pf);
+                s_last = atomicAdd(a.cnt + pf, 1u) == (unsigned)(pl - pf);
                 __threadfence();
             }
             __syncthreads();
             if (s_last) {
                 merge_slots(a, x, u, pf, pl - pf + 1, red);
-                if (tid == 0) a.cnt[u] = 0;
+                if (tid == 0) a.cnt[pf] = 0;
             }
         }
         __syncthreads();   // the rings are written again by the next piece

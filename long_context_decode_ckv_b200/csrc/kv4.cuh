@@ -90,7 +90,7 @@ struct Kv4AttendArgs {
     const int32_t* n_rows;           // [U]
     int max_rows, S;
     float* part;                     // o [U + kKv4MaxCtas][NH][D], then (m, l) [U + kKv4MaxCtas][NH][2]
-    unsigned* cnt;                   // [U] arrivals, 0 between calls
+    unsigned* cnt;                   // [kKv4MaxCtas] arrivals, 0 between calls
     float* out;                      // [B][Hq][D]
     float* lse;                      // [B][Hq] or null
 };
