@@ -409,7 +409,8 @@ ckv_status ckv_attend_rows_static(const ckv_config* cfg, const void* q, const vo
  * names.  They run on cfg->device whatever device is current (restored on
  * return), only enqueue work on `stream`, allocate nothing and can be
  * captured into a graph.  n_max may be at most 2^31 - 1024, batch * n_q_heads at
- * most 2^20; pointers are 16-byte aligned.
+ * most 2^20; pointers are 16-byte aligned, those of positions, lengths, row
+ * lists and lse 4-byte.
  *
  * The 4-bit cache of K (or of V) is one buffer of ckv_kv4_bytes(cfg, group)
  * bytes, group 32, 64 or 128 neighbouring channels sharing a scale: codes

@@ -78,7 +78,8 @@ ckv_status attend(const ckv_config* cfg, int group, const void* q, const void* K
 {
     if (!valid_shape(cfg) || !valid_group(group) || !q || !K4 || !V4 || !workspace || !out) return CKV_ERR_INVALID_ARG;
     if (n < 1 || n > cfg->n_max) return CKV_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(K4, 16) || !aligned(V4, 16) || !aligned(workspace, 16) || !aligned(out, 16))
+    if (!aligned(q, 16) || !aligned(K4, 16) || !aligned(V4, 16) || !aligned(workspace, 16) || !aligned(out, 16) ||
+        !aligned(lens, 4) || !aligned(rows, 4) || !aligned(n_rows, 4) || !aligned(lse, 4))
         return CKV_ERR_INVALID_ARG;
     const int Gq = cfg->n_q_heads / cfg->n_kv_heads;
     const bool per_head = listed && cfg->mode == CKV_PER_HEAD;
@@ -151,7 +152,7 @@ CKV_API ckv_status ckv_qk_norm_rope(const ckv_config* cfg, const ckv_qkv* x, voi
         !valid_rows(x->v, x->v_stride, B, T, Hkv, esz) || !valid_rows(x->q_out, x->q_out_stride, B, T, Hq, esz))
         return CKV_ERR_INVALID_ARG;
     if (!aligned(x->K, 16) || !aligned(x->V, 16) || !aligned(x->K4, 16) || !aligned(x->V4, 16) ||
-        !aligned(x->q_weight, 16) || !aligned(x->k_weight, 16))
+        !aligned(x->q_weight, 16) || !aligned(x->k_weight, 16) || !aligned(x->pos, 4))
         return CKV_ERR_INVALID_ARG;
     ckv::QkvArgs a{};
     for (int i = 0; i < x->rot_dim / 2; ++i) {
@@ -202,7 +203,8 @@ CKV_API ckv_status ckv_kv4_write(const ckv_config* cfg, int group, const void* k
         return CKV_ERR_INVALID_ARG;
     const int esz = cfg->kv_dtype == CKV_BF16 ? 2 : 4;
     if (!valid_rows(k, k_stride_host, cfg->batch, n_tokens, cfg->n_kv_heads, esz) ||
-        !valid_rows(v, v_stride_host, cfg->batch, n_tokens, cfg->n_kv_heads, esz) || !aligned(K4, 16) || !aligned(V4, 16))
+        !valid_rows(v, v_stride_host, cfg->batch, n_tokens, cfg->n_kv_heads, esz) || !aligned(K4, 16) || !aligned(V4, 16) ||
+        !aligned(pos, 4))
         return CKV_ERR_INVALID_ARG;
     if (n_tokens == 0) return CKV_OK;
     ckv::QkvArgs a{};

@@ -38,3 +38,20 @@ def test_one_workspace_over_batches_of_different_size():
         cases[i].out.fill_(9.0)
         cases[i].lse.fill_(9.0)
         cases[i].run().check()
+
+
+# --------------------------------------------------------------- refusals
+def test_addresses_off_four_bytes_are_refused():
+    rng = np.random.default_rng(42)
+    rows = torch.full((2, 5), 9, dtype=torch.int32, device="cuda")
+    c = Case(rng, 1, 4, 2, 40, 33, 32, "bf16", lens=[33], sinks=4, rows=rows, n_rows=rows[:, 0].contiguous(), max_rows=5)
+    good = dict(cfg=c.cfg, group=32, q=c.q, K4=c.K4, V4=c.V4, n=33, lens=c.lens, workspace=c.work, out=c.out, lse=c.lse)
+    more = dict(good, rows=rows, n_rows=c.n_rows, max_rows=5)
+    for call, args in ((ckv.ckv_kv4_dense_decode, good), (ckv.ckv_kv4_attend_rows, more)):
+        for name in ("lens", "lse", "rows", "n_rows"):
+            if name in args:
+                with pytest.raises(ckv.CkvError) as e:
+                    call(**{**args, name: args[name].data_ptr() + 2})
+                assert e.value.status == ckv.CKV_ERR_INVALID_ARG
+        call(**{**args, "lse": c.lse.data_ptr(), "lens": c.lens.data_ptr()})
+    c.check()

@@ -228,3 +228,20 @@ def test_reference_format_round_trip():
             c, scale, middle = ref.quantise(x, group)
             bound = np.repeat(scale / 2 + 2.0 ** -9 * np.abs(middle), group, -1)
             assert (np.abs(got - x) <= bound * (1 + 1e-12)).all()
+
+
+def test_integers_and_lse_on_four_bytes(L):
+    # a kernel faults on an address off its type's alignment, so the call refuses it
+    c, s, off = config(device=63), (ctypes.c_int64 * 3)(4096, 1024, 128), ctypes.c_void_p(4098)
+    C = ctypes.byref
+    assert L.ckv_qk_norm_rope(C(c), C(qkv(n_tokens=0)), None) == ckv.CKV_OK
+    assert L.ckv_qk_norm_rope(C(c), C(qkv(n_tokens=0, pos=off)), None) == BAD
+    write = [C(c), 32, P, s, P, s, 0, P, P, P, None]
+    assert L.ckv_kv4_write(*write) == ckv.CKV_OK
+    assert L.ckv_kv4_write(*write[:7], off, *write[8:]) == BAD
+    for i in (6, 9):
+        dense = [C(c), 32, P, P, P, 100, P, P, P, P, None]
+        assert L.ckv_kv4_dense_decode(*[off if k == i else x for k, x in enumerate(dense)]) == BAD
+    for i in (6, 7, 8, 12):
+        rows = [C(c), 32, P, P, P, 100, P, P, P, 16, P, P, P, None]
+        assert L.ckv_kv4_attend_rows(*[off if k == i else x for k, x in enumerate(rows)]) == BAD
