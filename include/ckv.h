@@ -499,8 +499,10 @@ size_t ckv_kv4_workspace(const ckv_config* cfg);           /* 0 for a bad argume
  * behind len_b are never used.  q [B][H_q][D] (kv_dtype), out [B][H_q][D] and
  * lse [B][H_q] (may be null) float32, device.  What 32-bit arithmetic would
  * not do: q enters the logits as 28-bit fixed point of its head's largest
- * channel, weights below 2^-34 of the largest count as zero in the output, and
- * a value scale keeps its 8 bits down to 2^-18 of the largest of its group.
+ * channel; a weight enters the sum over the values with 22 bits, and with an
+ * error of at most 2^-47 of the largest weight (22 bits down to 2^-24 of it);
+ * a value scale keeps its 8 bits down to 2^-29 of the largest of its group of
+ * channels in the sequence.
  * Supported for H_q / H_kv <= 8.
  * Errors: CKV_ERR_INVALID_ARG (also n outside [1, n_max]), CKV_ERR_CUDA. */
 ckv_status ckv_kv4_dense_decode(const ckv_config* cfg, int group, const void* q, const void* K4, const void* V4,

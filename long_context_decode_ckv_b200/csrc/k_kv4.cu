@@ -6,22 +6,28 @@
 // the rows, out = sum_j p_j v_j, lse = m + ln(l).  With c the codes, s the
 // scales and m the middles of a row's groups G,
 //   q.k = sum_G s_G (q_G.c_G) + m_G sum(q_G),
-//   sum_j p_j v_j = sum_j (p_j s_jG) c_jG + sum_j p_j m_jG per group G,
-// so the codes go to the tensor cores as they are and the scales are applied
-// to 4 logits a lane, not to 128 channels a row.  Both products are exact but
-// for the rounding of their float operands and sums:
+//   sum_j p_j v_j = sum_j p_j (s_jG c_jG) + sum_j p_j m_jG per group G,
+// so the keys' codes go to the tensor cores as they are and their scales are
+// applied to 4 logits a lane, not to 128 channels a row.  Both products are
+// exact but for the rounding of their float operands and sums:
 //   q.c on the 8-bit integer MMA: q as 28-bit fixed point of its head's
 //     largest channel, four signed base-128 digits in the rows of A (4 heads x
 //     4 digits), a nibble in the high half of a byte as the code times 16;
 //     unpacking 8 codes takes 3 instructions and no conversion.
-//   (p s).c on the fp16 MMA: codes as fp16 integers, p s as two fp16 parts
-//     (22 bits) in the 8 columns of B (4 heads x 2 parts).  p, 2^9 for the
-//     largest weight, is split once into p1 + p2, and a scale, times a power
-//     of two c_G that keeps the largest below 2, has 8 bits: h = fp16(p1 s),
-//     and the second part p1 s - h + p2 s is two fused fp16 operations, the
-//     first one exact.
-//     What a weight loses is below 2^-34 of the largest one, and a scale keeps
-//     its 8 bits down to 2^-18 of the largest of its group.
+//   p.(s c) on the fp16 MMA: a scale has 8 bits and a code at most 3 (or is
+//     -8), so s c is an fp16 number, exactly, once s is brought into fp16's
+//     range by a power of two c_G that keeps the largest of its group below
+//     2^13.  p, 2^9 for the largest weight, is two fp16 numbers in the 8
+//     columns of B (4 heads x 2 parts): p1 = fp16(p) and 2^13 (p - p1), whose
+//     sums are put together when the piece ends.  So a weight has 22 bits down
+//     to 2^-24 of the largest one and loses at most 2^-47 of that (half of
+//     fp16's last step, 2^-25, over 2^13 and 2^9), and a scale keeps its 8 bits
+//     down to 2^-29 of the largest of its group.  Scales multiplied into the
+//     weights' parts, both without the factor 2^13, take fewer instructions
+//     in groups of 64 and 128 (148 us instead of 156 and 139 instead of 149
+//     at the size below; 167 instead of 170 in groups of 32), but weights and
+//     scales then share one range: a weight 2^-20 of the largest keeps 14
+//     bits, and with a scale 2^-17 of the largest none.
 //
 // Work split: one unit per (batch, KV head), or per row list.  Units' tiles of
 // 32 rows are laid end to end and split evenly over the grid; a CTA's share
@@ -32,8 +38,8 @@
 // which one that is.
 //
 // Bound: instruction issue.  32 units of 131072 rows in groups of 32 (671 MB):
-// 162 us, 4.16 TB/s, 466 instructions for 16 rows of a warp at 69 % of the issue
-// slots, where the memory would take 103 us; groups of 128: 128 us.
+// 170 us, 3.94 TB/s, where the memory would take 103 us; groups of 64: 156 us, of
+// 128: 149 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -162,12 +168,6 @@ __device__ __forceinline__ uint32_t codes_high(uint32_t x, uint32_t magic, uint3
 // and the compiler, which cannot see through the shuffle, would otherwise
 // rebuild the other one at every use
 __device__ __forceinline__ uint32_t held(uint32_t v) { return __shfl_sync(kFull, v, 0); }
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -232,6 +232,10 @@ constexpr int kWarpSmem = (kStages * Stage<NG>::bytes + Unpacked<NG>::bytes + 12
 // when the reference was set, at most 2^kMost before it is set again (a new
 // maximum moves it only then; each move costs a pass over the sums).
 constexpr float kRef = 9.f, kMost = 14.f;
+// What a weight's second part is multiplied by (p <= 2^14 leaves p - p1 <= 4, so
+// the part stays below fp16's 65504), and the border that value scales are kept
+// below (8 times the largest 8-bit number under it is 65280).
+constexpr float kSecond = 8192.f, kTopScale = 8192.f;
 
 // NG: groups of a row.  NT: blocks of 4 query heads.  A lane is (g, t) =
 // (lane / 4, lane % 4).
@@ -244,7 +248,7 @@ struct Warp {
     float F[NT];             // logit (in powers of two) of one such unit
     float m[NT], l[NT];      // kRef - the maximum referred to, and this lane's share of the sum: head 4 nt + g % 4
     float Z[NT][NGH];        // this lane's share of sum p * middle
-    float acc[NT][8][4];     // sum (p s c_G) code: [channel block J, pair of channels][..]
+    float acc[NT][8][4];     // sum (p's part) (s c_G code): [channel block J, pair of channels][..]
     uint32_t magic, offset;  // of codes_low and codes_high
     int base[4];             // what integer sums start at
     float c[NG];             // the powers of two c_G
@@ -343,7 +347,7 @@ struct Warp {
 #pragma unroll
         for (int i = 0; i < 4; ++i) base[i] = (int)held(0x4b400000u);
 #pragma unroll
-        for (int j = 0; j < NG; ++j) c[j] = 1.2676506e30f;      // 2^100: scales below 2^-99
+        for (int j = 0; j < NG; ++j) c[j] = 5.1922969e33f;      // 2^112: scales below 2^-99
     }
 
     // ---- larger value scales than so far (this lane's row has sc): c_G down, sums with it
@@ -355,7 +359,7 @@ struct Warp {
             // scale < 2^e; the format's scales are below 2^126
             int e = (int)((most >> 23) & 255u) - 126;
             e = e < -99 ? -99 : e > 126 ? 126 : e;
-            const float now = fminf(c[j], __uint_as_float((uint32_t)(127 + 1 - e) << 23)), f = now / c[j];
+            const float now = fminf(c[j], __uint_as_float((uint32_t)(127 + 13 - e) << 23)), f = now / c[j];
             c[j] = now;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -386,7 +390,7 @@ struct Warp {
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             sc[j] = scale_of(vw.w[j]);
-            more |= sc[j] * c[j] >= 2.f;
+            more |= sc[j] * c[j] >= kTopScale;
         }
         if (__any_sync(kFull, more)) raise(sc);
         // the pair (columns 2 t', 2 t' + 1) that the row belongs to, and which of the two it is
@@ -511,13 +515,11 @@ struct Warp {
                 }
             }
         }
-        // ---- weights, and their products with the scales: this lane's column
-        // of B holds the first parts (g < 4) or the second ones.  With (a, b, d) =
-        // (p1, 0, 0) or (-p1, p1, p2), both are d s + (b s + fp16(a s)).
-        uint32_t pb[NT][NG][2];
+        // ---- weights: this lane's column of B holds the first parts (g < 4) or
+        // the second ones, (p - 0) 1 or (p - p1) 2^13
+        uint32_t pb[NT][2];
         {
-            uint32_t wa[NT][2], wb[NT][2], wd[NT][2];
-            const uint32_t second = g < 4 ? 0u : 0xffffffffu;
+            const float minus = g < 4 ? 0.f : -1.f, times = g < 4 ? 1.f : kSecond;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
@@ -526,12 +528,8 @@ struct Warp {
                 l[nt] += (p[0] + p[1]) + (p[2] + p[3]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t p1 = pack_f16(p[2 * k], p[2 * k + 1]);
-                    const float2 f = unpack_f16(p1);
-                    const uint32_t p2 = pack_f16(p[2 * k] - f.x, p[2 * k + 1] - f.y);
-                    wa[nt][k] = p1 ^ (second & 0x80008000u);
-                    wb[nt][k] = p1 & second;
-                    wd[nt][k] = p2 & second;
+                    const float2 f = unpack_f16(pack_f16(p[2 * k], p[2 * k + 1]));
+                    pb[nt][k] = pack_f16(fmaf(minus, f.x, p[2 * k]) * times, fmaf(minus, f.y, p[2 * k + 1]) * times);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -540,28 +538,23 @@ struct Warp {
                     for (int j = 0; j < NGH; ++j) Z[nt][j] = fmaf(p[e], __uint_as_float(h.w[j]), Z[nt][j]);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const Words<NG> vs = lds<NG>(un + U::VS + (8 * sub + t + 4 * k) * (4 * NG));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < NG; ++j)
-                        pb[nt][j][k] = fma2(wd[nt][k], vs.w[j], fma2(wb[nt][k], vs.w[j], mul2(wa[nt][k], vs.w[j])));
-            }
         }
-        // A is 16 channels x 16 rows
+        // A is 16 channels x 16 rows: codes times their rows' scales
+        Words<NG> vs[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) vs[k] = lds<NG>(un + U::VS + (8 * sub + t + 4 * k) * (4 * NG));
 #pragma unroll
         for (int J = 0; J < 4; ++J) {
             const uint32_t sel = J & 1 ? 0x7632u : 0x5410u;
             uint32_t x = __byte_perm(v[0].w[J >> 1], v[1].w[J >> 1], sel), y = __byte_perm(v[2].w[J >> 1], v[3].w[J >> 1], sel);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t a0 = codes_low(x, magic), a1 = codes_high(x, magic, offset);
-                const uint32_t a2 = codes_low(y, magic), a3 = codes_high(y, magic, offset);
+                const uint32_t sx = vs[0].w[J * NG / 4], sy = vs[1].w[J * NG / 4];
+                const uint32_t a0 = mul2(codes_low(x, magic), sx), a1 = mul2(codes_high(x, magic, offset), sx);
+                const uint32_t a2 = mul2(codes_low(y, magic), sy), a3 = mul2(codes_high(y, magic, offset), sy);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(acc[nt][2 * J + k], a0, a1, a2, a3, pb[nt][J * NG / 4][0], pb[nt][J * NG / 4][1]);
+                    mma_f16(acc[nt][2 * J + k], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                 x >>= 8;
                 y >>= 8;
             }
@@ -576,14 +569,14 @@ struct Warp {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int J = 0; J < 4; ++J) {
-                const float inv = 1.f / c[J * NG / 4];
+                const float inv = 1.f / c[J * NG / 4] * (t < 2 ? 1.f : 1.f / kSecond);   // columns of first or second parts
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        float v = acc[nt][2 * J + k][r];
-                        v += __shfl_xor_sync(kFull, v, 2);     // first and second part
-                        if (t < 2) red[(4 * nt + 2 * t + (r & 1)) * kRed + 32 * J + 4 * g + 2 * k + (r >> 1)] = v * inv;
+                        float v = acc[nt][2 * J + k][r] * inv;
+                        v += __shfl_xor_sync(kFull, v, 2);
+                        if (t < 2) red[(4 * nt + 2 * t + (r & 1)) * kRed + 32 * J + 4 * g + 2 * k + (r >> 1)] = v;
                     }
             }
             float s = l[nt];

@@ -8,7 +8,9 @@ import torch
 
 import long_context_decode_ckv_b200 as ckv
 from long_context_decode_ckv_b200 import build as ckv_build
+from tests import kv4_reference as ref
 from tests.conftest import gpu_available
+from tests.kv4_reference import D
 from tests.test_gpu_kv4 import Case
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a CUDA device")]
@@ -55,3 +57,58 @@ def test_addresses_off_four_bytes_are_refused():
                 assert e.value.status == ckv.CKV_ERR_INVALID_ARG
         call(**{**args, "lse": c.lse.data_ptr(), "lens": c.lens.data_ptr()})
     c.check()
+
+
+# ------------------------------------------------ weights and value scales
+def crafted(rng, gaps, vrows, group, dtype="f32", heads=4):
+    """One sequence whose row j has a weight of about 2^-gaps[j] of the largest and the values vrows[j]."""
+    n = len(gaps)
+    w = np.where(rng.random(D) < 0.5, -1.0, 1.0)
+    c = Case(rng, 1, heads, 1, n, n, group, dtype)
+    a = -np.asarray(gaps, np.float64) * np.log(2) / np.sqrt(D)
+    c.K4 = ref.cache_of((a[:, None] * w).astype(np.float32)[None, None], group, False, n).cuda()
+    c.V4 = ref.cache_of(vrows.astype(np.float32)[None, None], group, True, n).cuda()
+    c.q = torch.from_numpy((w * (1 + 0.01 * rng.standard_normal((1, heads, D)))).astype(np.float32)).to(c.dt).cuda()
+    return c
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("heads", [1, 4, 8])
+@pytest.mark.parametrize("gap", [4, 12, 20, 24])
+def test_many_small_weights_beside_a_few_that_take_nearly_all(gap, heads, group):
+    # the large weights' values are zero, or 2^-10 of the others', so that the output is made by the small weights: each of them
+    # has to enter with the same relative error as a large one
+    rng = np.random.default_rng(gap + heads)
+    n = 900
+    for small in (0.0, 2.0 ** -10):
+        gaps = gap + rng.uniform(-1, 1, n)
+        v = rng.standard_normal((n, D))
+        gaps[::32] = 0                                  # one in every tile of every warp
+        v[::32] *= small
+        crafted(rng, gaps, v, group, heads=heads).run().check()
+
+
+@pytest.mark.parametrize("order", ["first", "last", "mixed"])
+@pytest.mark.parametrize("gap,ratio", [(0, 6), (0, 17), (17, 14), (20, 17), (17, 10), (24, 6), (10, 28)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_rows_whose_values_differ_in_size(group, gap, ratio, order):
+    # a few rows of values 2^ratio times the others' and of no weight to speak of, before, behind or among rows of weight 2^-gap
+    # of the largest, whose own values are zero
+    rng = np.random.default_rng(ratio + gap)
+    n = 1024
+    gaps = gap + rng.uniform(-1, 1, n)
+    v = rng.standard_normal((n, D)) * 2.0 ** -ratio
+    gaps[5::32] = 0
+    v[5::32] = 0
+    large = {"first": np.arange(0, 256, 32), "last": np.arange(n - 256, n, 32), "mixed": np.arange(0, n, 96)}[order] + 9
+    gaps[large] = gap + ratio + 40
+    v[large] *= 2.0 ** ratio
+    crafted(rng, gaps, v, group).run().check()
+
+
+def test_large_values_of_small_weight_and_small_values_of_large_weight():
+    # p v is of the same size in every row, p between 1 and 2^-20
+    rng = np.random.default_rng(43)
+    n = 700
+    gaps = rng.uniform(0, 20, n)
+    crafted(rng, gaps, rng.standard_normal((n, D)) * 2.0 ** (gaps[:, None] - 20), 32).run().check()
