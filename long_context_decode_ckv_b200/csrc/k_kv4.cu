@@ -499,7 +499,10 @@ struct Warp {
                 float mx = fmaxf(fmaxf(z[nt][0], z[nt][1]), fmaxf(z[nt][2], z[nt][3]));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-                const float mn = fminf(m[nt], kRef - mx), f = ex2(mn - m[nt]);
+                // rounded down: where logits step by 16 (from 2^27 on), to
+                // nearest would leave 2^16 for the largest weight, which fp16
+                // does not hold
+                const float mn = fminf(m[nt], __fsub_rd(kRef, mx)), f = ex2(mn - m[nt]);
                 m[nt] = mn;
                 l[nt] *= f;
 #pragma unroll

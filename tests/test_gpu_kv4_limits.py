@@ -10,8 +10,8 @@ import long_context_decode_ckv_b200 as ckv
 from long_context_decode_ckv_b200 import build as ckv_build
 from tests import kv4_reference as ref
 from tests.conftest import gpu_available
-from tests.kv4_reference import D
-from tests.test_gpu_kv4 import Case
+from tests.kv4_reference import D, U32
+from tests.test_gpu_kv4 import Case, f64
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a CUDA device")]
 
@@ -112,3 +112,32 @@ def test_large_values_of_small_weight_and_small_values_of_large_weight():
     n = 700
     gaps = rng.uniform(0, 20, n)
     crafted(rng, gaps, rng.standard_normal((n, D)) * 2.0 ** (gaps[:, None] - 20), 32).run().check()
+
+
+# ------------------------------------------------------- logits far from 0
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("top", [1e6, 5e7, 9.4e7, 1.5e8, 1.8e8, 4e8, 1e10])
+def test_large_logits(top, sign):
+    # the largest logit, of size `top`, is far enough from the others for any error of 32 bits: it takes all the weight
+    rng = np.random.default_rng(44)
+    n, best = 300, 211
+    c = Case(rng, 1, 4, 1, n, n, 64, "f32")
+    w = np.where(rng.random(D) < 0.5, -1.0, 1.0)
+    size = rng.uniform(0.5, 0.9, n) if sign > 0 else -rng.uniform(1.1, 1.6, n)
+    size[best] = sign
+    c.q = torch.from_numpy(np.tile(w, (1, 4, 1)).astype(np.float32)).cuda() * 128.0
+    k = (size[:, None] * w * top / (128 * np.sqrt(D))).astype(np.float32)
+    c.K4 = ref.cache_of(k[None, None], 64, False, n).cuda()
+    c.run()
+    K = ref.values_of(c.K4, 1, 1, n, 64, False)[0, 0]
+    V = ref.values_of(c.V4, 1, 1, n, 64, True)[0, 0]
+    z = f64(c.q[0]) @ K[:n].T / np.sqrt(D)
+    order = np.sort(z, -1)
+    assert (z.argmax(-1) == best).all() and (order[:, -1] - order[:, -2] > 0.05 * top).all()
+    # the weight is 1 but for its two fp16 parts (2^-22), and the value is put together from its two terms (2 half steps)
+    parts = ref.parts_of(c.V4, 1, 1, n, 64, True)[0, 0][best]
+    assert (np.abs(f64(c.out[0]) - V[best]) <= 2.0 ** -21 * parts).all()
+    # the logit's error as in kv4_reference.attend, and its conversion to and from powers of two (4 half steps)
+    parts = ref.parts_of(c.K4, 1, 1, n, 64, False)[0, 0][best]
+    bound = (16 * U32 + 2.0 ** -27) * np.abs(f64(c.q[0])).max() * parts.sum() / np.sqrt(D) + 8 * U32 * top
+    assert (np.abs(f64(c.lse[0]) - z.max(-1)) <= bound).all()
