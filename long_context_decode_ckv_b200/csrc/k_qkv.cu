@@ -391,6 +391,7 @@ struct Rotation {
         if (a.interleaved) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (channel(threadIdx.x & 15, 2 * i) >= a.rot) continue;   // kept as they are, an infinity or a NaN too
                 const float u = x[2 * i], v = x[2 * i + 1];
                 x[2 * i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(v, s[i]));
                 x[2 * i + 1] = __fadd_rn(__fmul_rn(v, c[i]), __fmul_rn(u, s[i]));

@@ -11,7 +11,7 @@ from long_context_decode_ckv_b200 import build as ckv_build
 from tests import kv4_reference as ref
 from tests.conftest import gpu_available
 from tests.kv4_reference import D, U32
-from tests.test_gpu_kv4 import Case, f64
+from tests.test_gpu_kv4 import Case, config, f64
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a CUDA device")]
 
@@ -141,3 +141,46 @@ def test_large_logits(top, sign):
     parts = ref.parts_of(c.K4, 1, 1, n, 64, False)[0, 0][best]
     bound = (16 * U32 + 2.0 ** -27) * np.abs(f64(c.q[0])).max() * parts.sum() / np.sqrt(D) + 8 * U32 * top
     assert (np.abs(f64(c.lse[0]) - z.max(-1)) <= bound).all()
+
+
+# ------------------------------------------- channels that are not rotated
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [16, 64, 112])
+def test_channels_behind_the_rotation_stay(rot, interleaved, dtype):
+    # without a norm they keep their bits: infinities, NaN and -0 among them, and their neighbours are not touched
+    rng = np.random.default_rng(rot)
+    B, T, Hq, Hkv, n_max, group = 2, 9, 3, 1, 20, 32
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    c = config(B, Hq, Hkv, n_max, dt)
+    x = torch.from_numpy(rng.standard_normal((B, T, Hq + 2 * Hkv, D)).astype(np.float32)).to(dt)
+    x[:, 0, :, rot] = float("inf")
+    x[:, 1, :, rot + 1] = float("-inf")
+    x[:, 2, :, D - 1] = float("nan")
+    x[:, 3, :, rot::2] = -0.0
+    x[:, 4, :, rot + 1::2] = -0.0
+    x[:, 5, :, rot:] = -0.0
+    x = x.cuda()
+    pos = torch.arange(3, T + 3, dtype=torch.int32, device="cuda").repeat(B, 1)
+    freq = 1.0e4 ** (-np.arange(0, rot, 2) / rot)
+    bits = torch.int16 if dt == torch.bfloat16 else torch.int32
+    out = torch.zeros((B, T, Hq, D), dtype=dt, device="cuda")
+    K, V = (torch.zeros((B, Hkv, n_max, D), dtype=dt, device="cuda") for _ in range(2))
+    four = [torch.zeros(ckv.ckv_kv4_bytes(c, group), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want4 = [torch.zeros_like(b) for b in four]
+    q, k, v = x[:, :, :Hq], x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+    ckv.ckv_qk_norm_rope(c, q, k, v, pos, out, freq, interleaved=interleaved, K=K, V=V)
+
+    def same(got, want):
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got.view(bits)[~nan], want.view(bits)[~nan])
+    same(out[..., rot:].contiguous(), q[..., rot:].contiguous())
+    same(K[:, :, 3:T + 3, rot:].contiguous(), k[..., rot:].transpose(1, 2).contiguous())
+    assert torch.isfinite(out[..., :rot]).all() and torch.isfinite(K[..., :rot]).all()
+    # the 4-bit rows are those of K, quantised
+    out2 = torch.zeros_like(out)
+    ckv.ckv_qk_norm_rope(c, q, k, v, pos, out2, freq, interleaved=interleaved, K4=four[0], V4=four[1], group=group)
+    ckv.ckv_kv4_write(c, group, K[:, :, 3:T + 3].transpose(1, 2), V[:, :, 3:T + 3].transpose(1, 2), pos, *want4)
+    assert torch.equal(four[0], want4[0]) and torch.equal(four[1], want4[1])
+    same(out2, out)
