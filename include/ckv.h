@@ -448,7 +448,8 @@ size_t ckv_kv4_bytes(const ckv_config* cfg, int group);   /* 0 for a bad argumen
  * Errors: CKV_ERR_INVALID_ARG (also: K without V, K4 without V4, no cache at
  * all, an inv_freq that is not finite), CKV_ERR_CUDA. */
 typedef struct {
-    int n_tokens;                    /* T >= 0 tokens of each sequence                      */
+    int n_tokens;                    /* T >= 0 tokens of each sequence (0: the pointers to  */
+                                     /* rows and positions may be null)                     */
     int rot_dim;                     /* rotated channels: 0, 16, .., 128                    */
     int interleaved;                 /* pairs (2i, 2i+1) instead of (i, i + rot_dim/2)      */
     int group;                       /* of the 4-bit caches                                 */

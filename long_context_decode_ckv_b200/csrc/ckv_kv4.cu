@@ -138,8 +138,10 @@ CKV_API size_t ckv_kv4_workspace(const ckv_config* cfg)
 
 CKV_API ckv_status ckv_qk_norm_rope(const ckv_config* cfg, const ckv_qkv* x, void* stream)
 {
-    if (!valid_shape(cfg) || !x || !x->q || !x->k || !x->v || !x->pos || !x->q_out) return CKV_ERR_INVALID_ARG;
+    if (!valid_shape(cfg) || !x) return CKV_ERR_INVALID_ARG;
     if (x->n_tokens < 0 || (int64_t)cfg->batch * x->n_tokens > INT32_MAX) return CKV_ERR_INVALID_ARG;
+    // an array of no tokens may have no address
+    if (x->n_tokens > 0 && (!x->q || !x->k || !x->v || !x->pos || !x->q_out)) return CKV_ERR_INVALID_ARG;
     if ((x->K == nullptr) != (x->V == nullptr) || (x->K4 == nullptr) != (x->V4 == nullptr)) return CKV_ERR_INVALID_ARG;
     if (!x->K && !x->K4) return CKV_ERR_INVALID_ARG;
     if (x->K4 && !valid_group(x->group)) return CKV_ERR_INVALID_ARG;
@@ -197,8 +199,9 @@ CKV_API ckv_status ckv_kv4_write(const ckv_config* cfg, int group, const void* k
                                  const void* v, const int64_t* v_stride_host, int n_tokens, const int32_t* pos,
                                  void* K4, void* V4, void* stream)
 {
-    if (!valid_shape(cfg) || !valid_group(group) || !k || !v || !k_stride_host || !v_stride_host || !K4 || !V4)
+    if (!valid_shape(cfg) || !valid_group(group) || !k_stride_host || !v_stride_host || !K4 || !V4)
         return CKV_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!k || !v)) return CKV_ERR_INVALID_ARG;
     if (n_tokens < 0 || (int64_t)cfg->batch * n_tokens > INT32_MAX || (!pos && n_tokens > cfg->n_max))
         return CKV_ERR_INVALID_ARG;
     const int esz = cfg->kv_dtype == CKV_BF16 ? 2 : 4;

@@ -245,3 +245,24 @@ def test_integers_and_lse_on_four_bytes(L):
     for i in (6, 7, 8, 12):
         rows = [C(c), 32, P, P, P, 100, P, P, P, 16, P, P, P, None]
         assert L.ckv_kv4_attend_rows(*[off if k == i else x for k, x in enumerate(rows)]) == BAD
+
+
+class EmptyTensor(FakeTensor):
+    """A tensor without elements has no address."""
+
+    def data_ptr(self):
+        return 0
+
+
+def test_no_tokens(L):
+    # a chunk of no tokens is an empty tensor, and nothing to do
+    c, E = config(), EmptyTensor
+    size = ckv.ckv_kv4_bytes(c, 32)
+    four = [FakeTensor((size,), torch.uint8) for _ in range(2)]
+    q, k, pos = E((2, 0, 8, 128)), E((2, 0, 2, 128)), E((2, 0), torch.int32)
+    ckv.ckv_qk_norm_rope(c, q, k, k, pos, q, np.ones(64), K4=four[0], V4=four[1], group=32)
+    ckv.ckv_kv4_write(c, 32, k, k, pos, *four)
+    ckv.ckv_kv4_write(c, 32, k, k, None, *four)
+    x = {name: None for name in ("q", "k", "v", "pos", "q_out")}
+    assert L.ckv_qk_norm_rope(ctypes.byref(c), ctypes.byref(qkv(n_tokens=0, **x)), None) == ckv.CKV_OK
+    assert L.ckv_qk_norm_rope(ctypes.byref(c), ctypes.byref(qkv(n_tokens=0, group=48, **x)), None) == BAD
