@@ -387,12 +387,17 @@ def ckv_dense_decode(ctx, q, K, V, n, out, lse=None, stream=None):
 _qkv_bytes = struct.Struct("@4i2f4P9q4P3q4P")                      # ckv_qkv
 
 
+class _Elements(dict):
+    def __missing__(self, kv_dtype):
+        raise ValueError(f"kv_dtype is {kv_dtype}, expected CKV_F32 or CKV_BF16")
+
+
 def _dtypes():
     """torch's (int32, float32, {kv_dtype: element type}); torch is imported by whoever holds its tensors."""
     global _dtypes_known
     if _dtypes_known is None:
         import torch
-        _dtypes_known = torch.int32, torch.float32, {CKV_F32: torch.float32, CKV_BF16: torch.bfloat16}
+        _dtypes_known = torch.int32, torch.float32, _Elements({CKV_F32: torch.float32, CKV_BF16: torch.bfloat16})
     return _dtypes_known
 
 
@@ -432,6 +437,14 @@ def _buffer(device, x, size):
     _refuse(device, x, f"a contiguous buffer of {size} bytes")
 
 
+def _tokens(device, x):
+    """T of rows [B][T][heads][D]."""
+    try:
+        return x.shape[1]
+    except (AttributeError, IndexError):
+        _refuse(device, x, "rows [B][T][heads][D]")
+
+
 def _rows4(device, x, dtype, shape):
     """Address and strides of rows [B][T][heads][D]: a CUDA tensor of that
     shape, its channels contiguous."""
@@ -462,7 +475,7 @@ def ckv_qk_norm_rope(cfg, q, k, v, pos, q_out, inv_freq_host, *, q_weight=None, 
     L, (i32, _, elems), c = _lib or lib(), _dtypes_known or _dtypes(), ctypes.byref(cfg)
     B, Hq, Hkv, D, dev = cfg.batch, cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.device
     elem = elems[cfg.kv_dtype]
-    T = k.shape[1]
+    T = _tokens(dev, k)
     rot, freq = 0, None
     if inv_freq_host is not None:
         freq, rot = _hostp(inv_freq_host), 2 * len(inv_freq_host)
@@ -502,7 +515,7 @@ def ckv_kv4_write(cfg, group, k, v, pos, K4, V4, stream=None):
     """Rows k, v (CUDA tensors [B][T][H_kv][D], any strides) into the 4-bit
     caches at pos [B][T] (None: 0 .. T-1)."""
     L, (i32, _, elems), c = _lib or lib(), _dtypes_known or _dtypes(), ctypes.byref(cfg)
-    dev, T, elem = cfg.device, k.shape[1], elems[cfg.kv_dtype]
+    dev, T, elem = cfg.device, _tokens(cfg.device, k), elems[cfg.kv_dtype]
     shape = (cfg.batch, T, cfg.n_kv_heads, cfg.head_dim)
     kp, ks = _rows4(dev, k, elem, shape)
     vp, vs = _rows4(dev, v, elem, shape)

@@ -266,3 +266,27 @@ def test_no_tokens(L):
     x = {name: None for name in ("q", "k", "v", "pos", "q_out")}
     assert L.ckv_qk_norm_rope(ctypes.byref(c), ctypes.byref(qkv(n_tokens=0, **x)), None) == ckv.CKV_OK
     assert L.ckv_qk_norm_rope(ctypes.byref(c), ctypes.byref(qkv(n_tokens=0, group=48, **x)), None) == BAD
+
+
+def test_binding_names_what_is_wrong_with_rows_and_types(L):
+    # the kinds of error that the other arguments raise
+    c, F, i32 = config(), FakeTensor, torch.int32
+    size = ckv.ckv_kv4_bytes(c, 32)
+    four = [F((size,), torch.uint8) for _ in range(2)]
+    q, k, pos = F((2, 3, 8, 128)), F((2, 3, 2, 128)), F((2, 3), i32)
+    for bad, error in ((None, TypeError), (4096, TypeError), (np.zeros((2, 3, 2, 128)), TypeError), (torch.zeros((2, 3, 2, 128)), TypeError),
+                       (F((128,)), ValueError), (F(()), ValueError)):
+        with pytest.raises(error):
+            ckv.ckv_qk_norm_rope(c, q, bad, k, pos, q, np.ones(64), K4=four[0], V4=four[1], group=32)
+        with pytest.raises(error):
+            ckv.ckv_kv4_write(c, 32, bad, k, pos, *four)
+    c = config(kv_dtype=7)
+    f32 = torch.float32
+    out, work = F((2, 8, 128), f32), F((1 << 20,), torch.uint8)
+    for call in (lambda: ckv.ckv_qk_norm_rope(c, q, k, k, pos, q, np.ones(64), K4=four[0], V4=four[1], group=32),
+                 lambda: ckv.ckv_kv4_write(c, 32, k, k, pos, *four),
+                 lambda: ckv.ckv_kv4_read(c, 32, *four, 0, 1, F((2, 2, 100, 128)), None),
+                 lambda: ckv.ckv_kv4_dense_decode(c, 32, F((2, 8, 128)), *four, 50, None, work, out),
+                 lambda: ckv.ckv_kv4_attend_rows(c, 32, F((2, 8, 128)), *four, 50, None, F((4, 16), i32), F((4,), i32), 16, work, out)):
+        with pytest.raises(ValueError):
+            call()
