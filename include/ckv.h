@@ -444,9 +444,11 @@ size_t ckv_kv4_bytes(const ckv_config* cfg, int group);   /* 0 for a bad argumen
  * sequence at the same position leave an unspecified mixture in that row.
  * Strides are in elements, for batch, token and head; channels are
  * contiguous; a multiple of 16 bytes each (where there is more than one).
- * q_out may be q (in place).
+ * q_out may be q (in place, the strides the same); otherwise what the call
+ * writes overlaps neither itself nor what it reads.
  * Errors: CKV_ERR_INVALID_ARG (also: K without V, K4 without V4, no cache at
- * all, an inv_freq that is not finite), CKV_ERR_CUDA. */
+ * all, an inv_freq that is not finite, a q_out of stride 0 or in place with
+ * other strides than q's), CKV_ERR_CUDA. */
 typedef struct {
     int n_tokens;                    /* T >= 0 tokens of each sequence (0: the pointers to  */
                                      /* rows and positions may be null)                     */

@@ -65,6 +65,17 @@ bool valid_rows(const void* p, const int64_t* stride, int batch, int tokens, int
     return true;
 }
 
+// rows that are written: no two at one address by a stride of zero, and where
+// they start with the rows that are read, they are those (in place)
+bool valid_out(const ckv_qkv* x, int batch, int tokens, int heads)
+{
+    const int size[3] = {batch, tokens, heads};
+    for (int i = 0; i < 3; ++i)
+        if (size[i] > 1 && (x->q_out_stride[i] == 0 || (x->q_out == x->q && x->q_out_stride[i] != x->q_stride[i])))
+            return false;
+    return true;
+}
+
 // The counters at the head of a workspace, as many for every configuration:
 // where they end may not depend on the call, since one call's partial results
 // would lie where the next one, of another batch, expects zeros.
@@ -151,7 +162,8 @@ CKV_API ckv_status ckv_qk_norm_rope(const ckv_config* cfg, const ckv_qkv* x, voi
     const int esz = cfg->kv_dtype == CKV_BF16 ? 2 : 4;
     const int B = cfg->batch, T = x->n_tokens, Hq = cfg->n_q_heads, Hkv = cfg->n_kv_heads;
     if (!valid_rows(x->q, x->q_stride, B, T, Hq, esz) || !valid_rows(x->k, x->k_stride, B, T, Hkv, esz) ||
-        !valid_rows(x->v, x->v_stride, B, T, Hkv, esz) || !valid_rows(x->q_out, x->q_out_stride, B, T, Hq, esz))
+        !valid_rows(x->v, x->v_stride, B, T, Hkv, esz) || !valid_rows(x->q_out, x->q_out_stride, B, T, Hq, esz) ||
+        !valid_out(x, B, T, Hq))
         return CKV_ERR_INVALID_ARG;
     if (!aligned(x->K, 16) || !aligned(x->V, 16) || !aligned(x->K4, 16) || !aligned(x->V4, 16) ||
         !aligned(x->q_weight, 16) || !aligned(x->k_weight, 16) || !aligned(x->pos, 4))

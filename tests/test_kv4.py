@@ -290,3 +290,17 @@ def test_binding_names_what_is_wrong_with_rows_and_types(L):
                  lambda: ckv.ckv_kv4_attend_rows(c, 32, F((2, 8, 128)), *four, 50, None, F((4, 16), i32), F((4,), i32), 16, work, out)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_queries_over_themselves(L):
+    # rows written by one warp while another still has to read them, or twice: refused, not raced
+    c = config()
+    Q, S3 = ctypes.c_void_p(8192), ctypes.c_int64 * 3
+    call = lambda **kw: L.ckv_qk_norm_rope(ctypes.byref(c), ctypes.byref(qkv(n_tokens=0, **kw)), None)  # noqa: E731
+    assert call() == ckv.CKV_OK                                          # in place
+    assert call(q_out=Q, q_out_stride=S3(4096, 1024, 256)) == ckv.CKV_OK  # elsewhere, other strides
+    for stride in ((8192, 1024, 128), (4096, 1024, 256)):
+        assert call(q_out_stride=S3(*stride)) == BAD
+    for stride in ((0, 1024, 128), (4096, 1024, 0)):
+        assert call(q_out=Q, q_out_stride=S3(*stride)) == BAD
+    assert call(q_out_stride=S3(4096, 0, 128)) == ckv.CKV_OK              # one that takes no part: there are no two tokens
