@@ -49,6 +49,7 @@ ckv_status device_sms(int device, int* sms)
 ckv_status status_of(cudaError_t e)
 {
     if (e == cudaSuccess) return CKV_OK;
+    cudaGetLastError();                                    // reported here, not again by the next call
     return e == cudaErrorInvalidValue ? CKV_ERR_INVALID_ARG : CKV_ERR_CUDA;
 }
 

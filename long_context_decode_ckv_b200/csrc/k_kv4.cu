@@ -944,8 +944,7 @@ cudaError_t launch_attend_t(const Kv4AttendArgs& a, int bf16, int sms, cudaStrea
         P = a.U * each;
         if (P > sms) P = a.U < sms ? sms / a.U * a.U : most;
     }
-    fn<<<(unsigned)P, kThreads, kWarps * kWarpSmem<NG>, st>>>(a, bf16);
-    return cudaGetLastError();
+    return launch_kernel(fn, dim3((unsigned)P), kThreads, kWarps * kWarpSmem<NG>, st, a, bf16);
 }
 
 template <bool ROWS>

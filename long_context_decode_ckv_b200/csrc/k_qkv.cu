@@ -627,8 +627,7 @@ cudaError_t launch_qkv_t(const QkvArgs& a, int sms, cudaStream_t st)
     const int64_t grid = (tokens * slices + kQkvWarps - 1) / kQkvWarps;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     auto fn = a.group == 0 ? k_qkv<BF16, 0> : a.group == 32 ? k_qkv<BF16, 32> : a.group == 64 ? k_qkv<BF16, 64> : k_qkv<BF16, 128>;
-    fn<<<(unsigned)grid, 32 * kQkvWarps, 0, st>>>(a, per_warp, slices);
-    return cudaGetLastError();
+    return launch_kernel(fn, dim3((unsigned)grid), 32 * kQkvWarps, 0, st, a, per_warp, slices);
 }
 
 template <bool BF16>
@@ -637,8 +636,7 @@ cudaError_t launch_read_t(const Kv4ReadArgs& a, cudaStream_t st)
     const int64_t y = a.units < 32768 ? a.units : 32768, z = (a.units + y - 1) / y;
     const dim3 grid((unsigned)((a.count - 1) / (16 * kReadRows) + 1), (unsigned)y, (unsigned)z);
     auto fn = a.group == 32 ? k_kv4_read<BF16, 32> : a.group == 64 ? k_kv4_read<BF16, 64> : k_kv4_read<BF16, 128>;
-    fn<<<grid, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(fn, grid, 256, 0, st, a);
 }
 
 }  // namespace

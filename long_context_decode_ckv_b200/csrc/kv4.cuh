@@ -29,6 +29,20 @@ constexpr int kRowCodes = kD / 2;              // code bytes of one row
 
 __host__ __device__ inline int64_t kv4_rows(int n_max) { return ((int64_t)n_max + 15) / 16 * 16; }
 
+// A launch's own status.  cudaGetLastError() after <<<>>> would also report,
+// as this call's, what an earlier call of the thread left behind (an
+// allocation that failed, for instance).
+template <class... Params, class... Args>
+cudaError_t launch_kernel(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const Args&... args)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    return cudaLaunchKernelEx(&c, fn, args...);
+}
+
 // one 4-bit cache as the kernels see it
 struct Kv4 {
     unsigned char* codes;    // [units][R][64]

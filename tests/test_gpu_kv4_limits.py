@@ -184,3 +184,26 @@ def test_channels_behind_the_rotation_stay(rot, interleaved, dtype):
     ckv.ckv_kv4_write(c, group, K[:, :, 3:T + 3].transpose(1, 2), V[:, :, 3:T + 3].transpose(1, 2), pos, *want4)
     assert torch.equal(four[0], want4[0]) and torch.equal(four[1], want4[1])
     same(out2, out)
+
+
+# ----------------------------------------------------- errors of other calls
+def test_calls_after_another_one_failed():
+    # an allocation of a terabyte fails at once; what it leaves behind is not an error of the calls that follow
+    rng = np.random.default_rng(46)
+    big = config(16, 64, 8, 1024, torch.bfloat16, sinks=4)
+    big.max_communities, big.kappa, big.budget, big.slack, big.pool_capacity = 16, 8, 64, 16, 2 ** 31 - 1
+    c = Case(rng, 1, 4, 2, 40, 33, 32, "bf16")
+    x = torch.randn((1, 5, 8, D), device="cuda").bfloat16()
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")[None].contiguous()
+    K, V = (torch.zeros((1, 2, 40, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    calls = [
+        lambda: ckv.ckv_qk_norm_rope(c.cfg, x[:, :, :4], x[:, :, 4:6], x[:, :, 6:], pos, x[:, :, :4], np.ones(64), K=K, V=V),
+        lambda: ckv.ckv_kv4_read(c.cfg, 32, c.K4, c.V4, 0, 40, K, V),
+        lambda: c.run().check(),
+        lambda: ckv.ckv_kv4_write(c.cfg, 32, x[:, :, 4:6], x[:, :, 6:], pos, c.K4, c.V4),
+    ]
+    for call in calls:
+        with pytest.raises(ckv.CkvError) as e:
+            ckv.ckv_create(big)
+        assert e.value.status == ckv.CKV_ERR_OOM
+        call()
