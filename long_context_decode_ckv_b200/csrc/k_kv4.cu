@@ -244,8 +244,9 @@ struct Warp {
     static constexpr int NGH = NG > 1 ? NG / 2 : 1;    // groups whose middles this lane's half (g / 4) sums
 
     uint32_t qa[NT][4][4];   // digits of q: A of the k32 step j
-    float qs[NT][NGH];       // sum of q over a group, in units of the lane's integer logit
-    float F[NT];             // logit (in powers of two) of one such unit
+    float qs[NT][NGH];       // this lane half's share of the sum of q over a group
+    float unit[NT], unit128[NT], off[NT];    // one step of the lane's second digit, of its first one, and minus the offsets of both
+    float F[NT];             // logit (in powers of two) of a product of 1
     float m[NT], l[NT];      // kRef - the maximum referred to, and this lane's share of the sum: head 4 nt + g % 4
     float Z[NT][NGH];        // this lane's share of sum p * middle
     float acc[NT][8][4];     // sum (p's part) (s c_G code): [channel block J, pair of channels][..]
@@ -322,8 +323,17 @@ struct Warp {
                 part += __shfl_xor_sync(kFull, part, 2);
                 sum[j] = (float)part;
             }
-            // a lane's integer logit counts units of 2^14 (first half) or 1, times 16 (the codes)
-            const float in_units = (g < 4 ? 1.f / 16384.f : 1.f) * 16.f * 4.f;
+            // a lane's integer logit counts 2^14 X (first half) or X, times 16
+            // (the codes).  It is turned into q.c itself, and not left in those
+            // units until the scales are applied: keys near the largest float
+            // would overflow with small q.  The power of two is kept where
+            // neither it nor the offsets leave the floats; F has the rest.
+            const int E = e - 27 + (g < 4 ? 10 : -4), kept = min(max(E, -100), 84);
+            unit[nt] = __uint_as_float((uint32_t)(127 + kept) << 23);
+            unit128[nt] = 128.f * unit[nt];
+            off[nt] = -129.f * 12582912.f * unit[nt];
+            // the middles' share: half of q's sum each where there is one group
+            const float in_units = (g < 4 ? 1.f / 16384.f : 1.f) * 64.f * unit[nt];
             if constexpr (NG == 4) {
                 qs[nt][0] = (g < 4 ? sum[0] : sum[2]) * in_units;
                 qs[nt][1] = (g < 4 ? sum[1] : sum[3]) * in_units;
@@ -332,7 +342,7 @@ struct Warp {
             } else {
                 qs[nt][0] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * (0.5f * in_units);
             }
-            F[nt] = bad ? NAN : 1.f / up1 / up2 * (kLog2Scale * (g < 4 ? 1024.f : 0.0625f));
+            F[nt] = bad ? NAN : kLog2Scale * __uint_as_float((uint32_t)(127 + E - kept) << 23);
             m[nt] = FLT_MAX;
             l[nt] = 0.f;
 #pragma unroll
@@ -445,8 +455,7 @@ struct Warp {
             // The sums start at the bits of 1.5 * 2^23, so that they are floats
             // 1.5 * 2^23 + v for |v| < 2^22: no conversion.  128 v0 + v1, the two
             // digits' sums, is then one FMA that also takes the offsets off
-            // (exact) and one add that rounds.
-            constexpr float kOff = -129.f * 12582912.f;
+            // (exact) and one that rounds.
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 const Words<4> w = lds<4>(st + S::K + (16 * sub + 8 * a + kr) * kRowCodes + 16 * t);
@@ -462,7 +471,7 @@ struct Warp {
                         if (j % per == per - 1) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const float v = fmaf(__int_as_float(d[nt][i]), 128.f, kOff) + __int_as_float(d[nt][2 + i]);
+                                const float v = fmaf(__int_as_float(d[nt][2 + i]), unit[nt], fmaf(__int_as_float(d[nt][i]), unit128[nt], off[nt]));
                                 z[nt][2 * a + i] = fmaf(ks[2 * a + i][j / per], v, z[nt][2 * a + i]);
                             }
                         }

@@ -207,3 +207,29 @@ def test_calls_after_another_one_failed():
             ckv.ckv_create(big)
         assert e.value.status == ckv.CKV_ERR_OOM
         call()
+
+
+# -------------------------------------------------- keys and queries far from 1
+@pytest.mark.parametrize("kexp,qexp", [(100, -100), (84, -80), (95, -90), (118, -110), (-100, 100), (-120, 120), (-60, 60), (105, -3),
+                                       (110, 10), (122, -122), (0, 115), (10, 100)])
+@pytest.mark.parametrize("group", [32, 128])
+def test_keys_and_queries_of_any_size(group, kexp, qexp):
+    rng = np.random.default_rng(45)
+    n = 200
+    c = Case(rng, 1, 4, 1, n, n, group, "f32")
+    k = rng.standard_normal((n, D)) + 0.5
+    q = rng.standard_normal((4, D))
+    c.K4 = ref.cache_of((k * 2.0 ** kexp).astype(np.float32)[None, None], group, False, n).cuda()
+    c.q = torch.from_numpy((q * 2.0 ** qexp).astype(np.float32))[None].cuda()
+    c.run()
+    if abs(kexp + qexp) <= 10:
+        c.check()
+        return
+    # logits of 2^20 and more: one row takes all the weight, 1 but for its two fp16 parts
+    K = ref.values_of(c.K4, 1, 1, n, group, False)[0, 0]
+    z = f64(c.q[0]) @ K[:n].T / np.sqrt(D)
+    order = np.sort(z, -1)
+    assert (order[:, -1] - order[:, -2] > 2.0 ** -10 * np.abs(z).max(-1)).all()
+    want = ref.values_of(c.V4, 1, 1, n, group, True)[0, 0][z.argmax(-1)]
+    parts = ref.parts_of(c.V4, 1, 1, n, group, True)[0, 0][z.argmax(-1)]
+    assert (np.abs(f64(c.out[0]) - want) <= 2.0 ** -21 * parts).all()
