@@ -245,7 +245,7 @@ struct Warp {
 
     uint32_t qa[NT][4][4];   // digits of q: A of the k32 step j
     float qs[NT][NGH];       // this lane half's share of the sum of q over a group
-    float unit[NT], unit128[NT], off[NT];    // one step of the lane's second digit, of its first one, and minus the offsets of both
+    float unit[NT], unit128[NT], zero[NT];   // one step of the lane's second digit, of its first one, and minus the offsets of both
     float F[NT];             // logit (in powers of two) of a product of 1
     float m[NT], l[NT];      // kRef - the maximum referred to, and this lane's share of the sum: head 4 nt + g % 4
     float Z[NT][NGH];        // this lane's share of sum p * middle
@@ -331,7 +331,7 @@ struct Warp {
             const int E = e - 27 + (g < 4 ? 10 : -4), kept = min(max(E, -100), 84);
             unit[nt] = __uint_as_float((uint32_t)(127 + kept) << 23);
             unit128[nt] = 128.f * unit[nt];
-            off[nt] = -129.f * 12582912.f * unit[nt];
+            zero[nt] = -129.f * 12582912.f * unit[nt];
             // the middles' share: half of q's sum each where there is one group
             const float in_units = (g < 4 ? 1.f / 16384.f : 1.f) * 64.f * unit[nt];
             if constexpr (NG == 4) {
@@ -471,7 +471,7 @@ struct Warp {
                         if (j % per == per - 1) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const float v = fmaf(__int_as_float(d[nt][2 + i]), unit[nt], fmaf(__int_as_float(d[nt][i]), unit128[nt], off[nt]));
+                                const float v = fmaf(__int_as_float(d[nt][2 + i]), unit[nt], fmaf(__int_as_float(d[nt][i]), unit128[nt], zero[nt]));
                                 z[nt][2 * a + i] = fmaf(ks[2 * a + i][j / per], v, z[nt][2 * a + i]);
                             }
                         }
@@ -926,6 +926,70 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
     }
 }
 
+// How many tiles the units of a call have: all `tiles` (dense, one length), at
+// most that and mostly near it (row lists), at most that (sequences of their
+// own lengths).
+enum Extent { kEqual, kLists, kLengths };
+
+// CTAs for U units; `most` of them run at once, `sms` of them with an SM each.
+// Measured at 4 heads, groups of 32, 148 SMs.
+//
+// Equal units: shares that end with units (k of them each), or as many shares
+// as CTAs run at once, wherever their borders fall.  Costs are in rounds of a
+// warp's tile, which take 1.6 us with one CTA on an SM and 1.7 times that
+// with two.  A merge through slots costs 2.2 rounds (3.7 with two CTAs on an
+// SM) and a little for each slot; borders within units 6 (7.2), since CTAs
+// then start, end and merge twice, and more for each further unit of a share; a
+// second wave of CTAs 3.5.  32 units of 1250 tiles take 60 us in 288 shares and 67
+// in 296, of 375 tiles 28 and 35; 80 of 118 tiles 26 us in 240 shares, 33 in 80
+// and 32 in 296; 112 of 73 tiles 24 in 112 and 30 in 296; 8 of 600 tiles 19 in
+// 144 and 22 in 296; 256 of 19 tiles 17 in 256 and 26 in 296.
+//
+// Lists and lengths: shares end with units only if these turn out equal, which
+// happens often enough that the number is a multiple of U where one covers the
+// machine (32 units of 150 tiles in 128 and 148 shares: equal ones 19 and 25
+// us, within a tenth of one another 27 and 26, lengths from an eighth on 23 and
+// 23).  A CTA for each unit while a warp has up to 3 tiles, then one CTA to an
+// SM, but two where U takes more than half of the SMs (80 units of 60 tiles in
+// 80, 148 and 240 shares: equal ones 21, 25 and 20 us, lengths apart 33, 28 and
+// 27; of 30 tiles 14, 22 and 16, and 28, 25 and 24: from 6 tiles a warp on) or a
+// warp has four tiles on the whole machine.  More units than SMs: two CTAs to
+// an SM, but a CTA for each list of a tile a warp (160 of 4: 12 us, 23 in 296).
+long long grid_of(long long U, long long tiles, Extent extent, long long sms, long long most)
+{
+    const long long total = U * tiles;
+    if (extent != kEqual) {
+        const long long each = tiles <= 3 * kWarps ? 1 : (tiles + kWarps - 1) / kWarps, aligned = U <= most ? most / U * U : 0;
+        if (total > most * kWarps * 4) return 20 * aligned >= 19 * most ? aligned : most;
+        if (U >= sms) return extent == kLists && U <= most && tiles <= kWarps ? U : most;
+        if (2 * U <= sms) return U * (each < sms / U ? each : sms / U);
+        if (each <= 6) return U;
+        return 4 * aligned >= 3 * most ? aligned : most;
+    }
+    const auto rounds = [](double t) { return t <= 4 * kWarps ? ceil(t / kWarps) : t / kWarps + 0.5; };
+    const auto pace = [&](long long ctas) { return ctas <= sms ? 1.0 : 1.7; };
+    const double over = (double)U / (double)most;
+    double best = rounds((double)total / (double)most) * pace(most) + (most > sms ? 7.2 : 6.0) + 0.02 / over +
+                  (over > 1.0 ? 8.0 * (over - 1.0) : 0.0);
+    long long P = most;
+    const auto offer = [&](long long k) {
+        if (k < 1 || U * k > (k == 1 ? kKv4MaxCtas : most)) return;
+        const long long waves = U * k / most, rest = U * k % most;
+        const double paces = (double)waves * pace(most) + (rest ? pace(rest) : 0.0);
+        double cost = rounds((double)((tiles + k - 1) / k)) * paces + 3.5 * (double)(waves + (rest != 0) - 1);
+        if (k > 1) cost += (U * k > sms ? 3.7 : 2.2) + 0.02 * (double)k;
+        if (cost < best) {
+            best = cost;
+            P = U * k;
+        }
+    };
+    offer(1);
+    for (int r = 1; r <= 4; ++r) offer((tiles + r * kWarps - 1) / (r * kWarps));
+    offer(sms / U);
+    offer(most / U);
+    return P;
+}
+
 template <int NG, int NT, bool ROWS>
 cudaError_t launch_attend_t(const Kv4AttendArgs& a, int bf16, int sms, cudaStream_t st)
 {
@@ -936,23 +1000,10 @@ cudaError_t launch_attend_t(const Kv4AttendArgs& a, int bf16, int sms, cudaStrea
         if (e != cudaSuccess) return e;
         prepared.fetch_or(uint64_t(1) << a.device, std::memory_order_release);
     }
-    // tiles of a unit, at most
     const long long tiles = ROWS ? ((long long)a.S + a.max_rows + 1 + kTile - 1) / kTile : (a.n + kTile - 1) / kTile;
+    const Extent extent = ROWS ? kLists : a.lens && a.B > 1 ? kLengths : kEqual;
     const long long most = kCtasPerSM<NT> * sms < kKv4MaxCtas ? kCtasPerSM<NT> * sms : kKv4MaxCtas;
-    // Few tiles: shares that start and end with units (where all are as long
-    // as the longest), a CTA for each unit while a warp has up to 3 tiles (a
-    // merge through slots costs about as much as two more: 32 tiles a unit of
-    // 8, 10.7 us, with one CTA each 12.8), and one CTA to an SM (32 units of
-    // 47 tiles 12.2 us, with more 13.9; 128 lists of 33 tiles 20.0 and 22.8, 32
-    // lists of 129 tiles 23.4 and 22.7).  Many tiles: the whole machine,
-    // wherever the shares' borders fall.
-    long long P = (long long)a.U * tiles;
-    if (P > most * kWarps * 4) P = most;
-    else {
-        const long long each = tiles <= 3 * kWarps ? 1 : (tiles + kWarps - 1) / kWarps;
-        P = a.U * each;
-        if (P > sms) P = a.U < sms ? sms / a.U * a.U : most;
-    }
+    const long long P = grid_of(a.U, tiles, extent, sms, most);
     return launch_kernel(fn, dim3((unsigned)P), kThreads, kWarps * kWarpSmem<NG>, st, a, bf16);
 }
 

@@ -233,3 +233,38 @@ def test_keys_and_queries_of_any_size(group, kexp, qexp):
     want = ref.values_of(c.V4, 1, 1, n, group, True)[0, 0][z.argmax(-1)]
     parts = ref.parts_of(c.V4, 1, 1, n, group, True)[0, 0][z.argmax(-1)]
     assert (np.abs(f64(c.out[0]) - want) <= 2.0 ** -21 * parts).all()
+
+
+# ------------------------------------------------------- splits of the work
+GRIDS = [
+    # B, Hq, Hkv, n, group, dtype, lens: units of one length in one share each, in several, in shares that cross units, in two
+    # waves of CTAs; units of their own lengths, a tile to a CTA, one CTA to an SM, two
+    (10, 32, 8, 3700, 32, "bf16", None),
+    (5, 4, 1, 20000, 128, "bf16", None),
+    (1, 2, 1, 33000, 64, "f32", None),
+    (7, 36, 9, 1500, 64, "bf16", None),
+    (25, 48, 12, 100, 128, "bf16", None),
+    (37, 16, 16, 70, 32, "f32", None),
+    (70, 20, 10, 40, 64, "bf16", None),
+    (20, 64, 8, 600, 128, "bf16", None),
+    (3, 8, 2, 1300, 32, "bf16", [1300, 11, 700]),
+    (12, 8, 8, 1200, 64, "f32", list(range(0, 1200, 100))),
+    (11, 32, 8, 4500, 128, "bf16", [4500 - 37 * i for i in range(11)]),
+    (90, 8, 8, 65, 32, "bf16", [i % 66 for i in range(90)]),
+]
+
+
+@pytest.mark.parametrize("case", GRIDS, ids=lambda c: "-".join(map(str, c[:6])) + ("-ragged" if c[6] else ""))
+def test_splits_of_the_work(case):
+    B, Hq, Hkv, n, group, dtype, lens = case
+    Case(np.random.default_rng(n), B, Hq, Hkv, n + 3, n, group, dtype, lens=lens).run().check()
+
+
+def test_splits_of_row_lists():
+    rng = np.random.default_rng(47)
+    for B, Hq, Hkv, n, max_rows, per_head in ((1, 4, 1, 40000, 30000, False), (5, 8, 4, 700, 200, True), (20, 16, 4, 400, 300, False),
+                                              (80, 4, 1, 3000, 2900, False), (50, 16, 4, 64, 20, True)):
+        G = B * (Hq if per_head else Hkv)
+        rows = torch.from_numpy(rng.integers(4, n - 1, (G, max_rows)).astype(np.int32)).cuda()
+        n_rows = torch.from_numpy(rng.integers(0, max_rows + 1, G).astype(np.int32)).cuda()
+        Case(rng, B, Hq, Hkv, n, n, 64, "bf16", sinks=4, rows=rows, n_rows=n_rows, max_rows=max_rows, per_head=per_head).run().check()
