@@ -268,3 +268,62 @@ def test_splits_of_row_lists():
         rows = torch.from_numpy(rng.integers(4, n - 1, (G, max_rows)).astype(np.int32)).cuda()
         n_rows = torch.from_numpy(rng.integers(0, max_rows + 1, G).astype(np.int32)).cuda()
         Case(rng, B, Hq, Hkv, n, n, 64, "bf16", sinks=4, rows=rows, n_rows=n_rows, max_rows=max_rows, per_head=per_head).run().check()
+
+
+# ------------------------------------------------------------ long caches
+def test_sums_over_a_long_cache():
+    # 32 units of 1.2 million rows, the last ones more than 2^31 bytes into the codes: all logits 0, values in 3000 rows from the
+    # first to the last.  The weights are equal, so the output is the values' sum over n.
+    B, H, n, group, T = 4, 8, 1_200_000, 128, 3000
+    cfg = config(B, 4 * H, H, n, torch.bfloat16)
+    size = ckv.ckv_kv4_bytes(cfg, group)
+    assert size > 2 ** 31
+    if torch.cuda.mem_get_info()[0] < 3 * size:
+        pytest.skip("not enough device memory")
+    K4, V4 = (torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(48)
+    pos = np.stack([np.concatenate([[0, n - 1], 1 + rng.permutation(n - 2)[:T - 2]]) for _ in range(B)]).astype(np.int32)
+    v = torch.from_numpy(rng.standard_normal((B, T, H, D)).astype(np.float32)).bfloat16().cuda()
+    ckv.ckv_kv4_write(cfg, group, torch.zeros_like(v), v, torch.from_numpy(pos).cuda(), K4, V4)
+    q = torch.randn((B, 4 * H, D), device="cuda").bfloat16()
+    out, lse = torch.empty((B, 4 * H, D), device="cuda"), torch.empty((B, 4 * H), device="cuda")
+    work = torch.zeros(ckv.ckv_kv4_workspace(cfg), dtype=torch.uint8, device="cuda")
+    ckv.ckv_kv4_dense_decode(cfg, group, q, K4, V4, n, None, work, out, lse)
+    code, scale, middle = ref.quantise(v.float().cpu().numpy(), group)
+    want = (middle + scale * code).sum(1) / n                            # one group to a row
+    parts = (np.abs(middle) + np.abs(scale * code)).sum(1) / n
+    # the weights' sum: a lane adds once for 16 rows of its warp, one of 8 of a share, and a unit has 4 shares at least; the
+    # values: a warp meets a few of the 3000 rows (those of value 0 add nothing), then come 8 warps and up to 37 shares: 64 half
+    # steps of the sum of all their sizes
+    chain = (n / (16 * 8 * 4) + 64) * U32
+    bound = 64 * U32 * parts + chain * np.abs(want)
+    err = np.abs(f64(out).reshape(B, H, 4, D) - want[:, :, None])
+    assert (err <= bound[:, :, None]).all(), (err / bound[:, :, None]).max()
+    assert (np.abs(f64(lse) - np.log(n)) <= chain + 2 * U32 * np.log(n)).all()
+
+
+# ------------------------------------------------------- the order of a sum
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_in_its_order_written_out(dtype):
+    # 32 sums of four neighbouring squares one after the other, these by halves; every step rounded to 32 bits.  The kernel for
+    # 4-bit rows holds a row's channels in other lanes and adds in the same order.
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    B, T, H = 2, 150, 3
+    cfg = config(B, H, H, T, dt)
+    gen = torch.Generator(device="cuda").manual_seed(49)
+    x = (2 * torch.randn((B, T, 3 * H, D), generator=gen, device="cuda")).to(dt)
+    w = (1 + 0.1 * torch.randn(D, generator=gen, device="cuda")).to(dt)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda").repeat(B, 1)
+    four = [torch.zeros(ckv.ckv_kv4_bytes(cfg, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    y = x[:, :, :2 * H].float()
+    s = (y * y).unflatten(-1, (32, 4))
+    s = ((s[..., 0] + s[..., 1]) + s[..., 2]) + s[..., 3]
+    while s.shape[-1] > 1:
+        s = s[..., :s.shape[-1] // 2] + s[..., s.shape[-1] // 2:]
+    want = (y * torch.rsqrt(s / D + 1e-6) * w.float()).to(dt)
+    for more in ({}, dict(K4=four[0], V4=four[1], group=64)):
+        out = torch.empty((B, T, H, D), dtype=dt, device="cuda")
+        K, V = (torch.empty((B, H, T, D), dtype=dt, device="cuda") for _ in range(2))
+        ckv.ckv_qk_norm_rope(cfg, x[:, :, :H], x[:, :, H:2 * H], x[:, :, 2 * H:], pos, out, None, q_weight=w, k_weight=w, K=K, V=V,
+                             **more)
+        assert torch.equal(out, want[:, :, :H]) and torch.equal(K.transpose(1, 2), want[:, :, H:])
