@@ -517,8 +517,13 @@ __device__ __forceinline__ void do_rows(const QkvArgs& a, const double* freq, in
                 float lo, hi;
                 uint32_t params, code[2];
                 raw.template extremes<GROUP>(x, lo, hi);
-                kv4_quantise<BF16, KIND == kValue>(x, lo, hi, params, code);
-                if (live) kv4_store<GROUP, KIND == kValue>(four, row4, l, code, params);
+                // not the lanes beside a last odd row: whatever their registers
+                // hold would take the warp through the 64-bit steps (2 x 88410
+                // rows of one head: 170 us, 70 without)
+                if (live) {
+                    kv4_quantise<BF16, KIND == kValue>(x, lo, hi, params, code);
+                    kv4_store<GROUP, KIND == kValue>(four, row4, l, code, params);
+                }
                 row4 += 2 * four.R;
             }
             left -= 2;

@@ -327,3 +327,32 @@ def test_norm_in_its_order_written_out(dtype):
         ckv.ckv_qk_norm_rope(cfg, x[:, :, :H], x[:, :, H:2 * H], x[:, :, 2 * H:], pos, out, None, q_weight=w, k_weight=w, K=K, V=V,
                              **more)
         assert torch.equal(out, want[:, :, :H]) and torch.equal(K.transpose(1, 2), want[:, :, H:])
+
+
+# ---------------------------------------------------- odd numbers of heads
+@pytest.mark.parametrize("heads", [1, 3, 9, 11])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_an_odd_number_of_heads(dtype, heads):
+    # half of a warp has no row of its own beside the last head; codes, parameters and rows are those of the formulas
+    rng = np.random.default_rng(heads)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    B, T = 3, 700
+    c = config(B, heads, heads, T, dt)
+    x = torch.from_numpy((rng.standard_normal((B, T, 3 * heads, D)) * 2.0 ** rng.integers(-3, 4, (B, T, 1, 1))).astype(np.float32))
+    x = x.to(dt).cuda()
+    q, k, v = x[:, :, :heads], x[:, :, heads:2 * heads], x[:, :, 2 * heads:]
+    pos = torch.arange(T, dtype=torch.int32, device="cuda").repeat(B, 1)
+    for group in (32, 64, 128):
+        K, V = (torch.full((B, heads, T, D), 5.0, dtype=dt, device="cuda") for _ in range(2))
+        four, alone = ([torch.zeros(ckv.ckv_kv4_bytes(c, group), dtype=torch.uint8, device="cuda") for _ in range(2)] for _ in range(2))
+        out = torch.full((B, T, heads, D), 5.0, dtype=dt, device="cuda")
+        ckv.ckv_qk_norm_rope(c, q, k, v, pos, out, None, K=K, V=V, K4=four[0], V4=four[1], group=group)
+        ckv.ckv_kv4_write(c, group, k, v, None, *alone)
+        assert torch.equal(out, q) and torch.equal(K.transpose(1, 2), k) and torch.equal(V.transpose(1, 2), v)
+        for i, t in enumerate((k, v)):
+            assert torch.equal(four[i], alone[i])
+            by, pa = ref.split(alone[i], B, heads, T, group)
+            code, scale, middle = ref.quantise(t.float().cpu().numpy().transpose(0, 2, 1, 3), group)
+            np.testing.assert_array_equal(ref.codes(by[:, :, :T], bool(i)), code)
+            np.testing.assert_array_equal(pa[:, :, :T, :, 0], scale)
+            np.testing.assert_array_equal(pa[:, :, :T, :, 1], middle)
