@@ -434,8 +434,9 @@ size_t ckv_kv4_bytes(const ckv_config* cfg, int group);   /* 0 for a bad argumen
  *   a' = rot_scale (a cos f - b sin f), b' = rot_scale (b cos f + a sin f)
  * for the rot_dim / 2 pairs (a, b) of channels (i, i + rot_dim / 2), or
  * (2 i, 2 i + 1) when interleaved, f = pos[b][t] * inv_freq[i]; channels from
- * rot_dim on stay y.  32-bit arithmetic with one rounding at the end; the
- * angle is formed and reduced in 64 bits.  v is taken as it is.
+ * rot_dim on stay y.  32-bit arithmetic with one rounding at the end (the
+ * squares too: a row with channels from about 2^60 on overflows them and
+ * becomes 0); the angle is formed and reduced in 64 bits.  v is taken as it is.
  * q goes to q_out, k and v to row pos[b][t] of the caches K and V
  * ([B][H_kv][n_max][D]), of the 4-bit caches K4 and V4, or of both (the
  * 4-bit rows then hold the rows of K and V, quantised; without K and V what
@@ -519,6 +520,8 @@ ckv_status ckv_kv4_dense_decode(const ckv_config* cfg, int group, const void* q,
  * device memory.  An entry outside [n_sinks, len_b - 1) is no row (-1 pads a
  * list); a row listed twice counts twice; n_rows is clamped to
  * [0, max_rows].  A sequence of len_b <= n_sinks positions attends to those.
+ * The lists are the caller's: ckv_decode_step reads 16/32-bit caches, and the
+ * rows that it selects stay in its context.
  * Errors: as ckv_kv4_dense_decode. */
 ckv_status ckv_kv4_attend_rows(const ckv_config* cfg, int group, const void* q, const void* K4, const void* V4,
                                int n, const int32_t* lens, const int32_t* rows, const int32_t* n_rows, int max_rows,

@@ -24,10 +24,10 @@
 //     fp16's last step, 2^-25, over 2^13 and 2^9), and a scale keeps its 8 bits
 //     down to 2^-29 of the largest of its group.  Scales multiplied into the
 //     weights' parts, both without the factor 2^13, take fewer instructions
-//     in groups of 64 and 128 (148 us instead of 156 and 139 instead of 149
-//     at the size below; 167 instead of 170 in groups of 32), but weights and
-//     scales then share one range: a weight 2^-20 of the largest keeps 14
-//     bits, and with a scale 2^-17 of the largest none.
+//     (2 % less time in groups of 32 at the size below, 5 % and 7 % in groups
+//     of 64 and 128), but weights and scales then share one range: a weight
+//     2^-20 of the largest keeps 14 bits, and with a scale 2^-17 of the largest
+//     none.
 //
 // Work split: one unit per (batch, KV head), or per row list.  Units' tiles of
 // 32 rows are laid end to end and split evenly over the grid; a CTA's share
@@ -37,9 +37,14 @@
 // to arrive merges the slots in their order, so the result does not depend on
 // which one that is.
 //
-// Bound: instruction issue.  32 units of 131072 rows in groups of 32 (671 MB):
-// 170 us, 3.94 TB/s, where the memory would take 103 us; groups of 64: 156 us, of
-// 128: 149 us.
+// Measured: 32 units of 131072 rows in groups of 32 (671 MB) take 169 us, 3.97
+// TB/s, where the memory would take 103; in groups of 64 148, of 128 140; with
+// eight heads of a KV head 253.  By length, 32 units of 16384, 32768, 65536,
+// 131072 and 262144 rows take 33, 52, 89, 168 and 340 us: about 14 us that do
+// not grow (start, queries, merge) and 1.2 us for 1000 rows, 1.3 beyond 131072.
+// What bounds the part that grows: 472 instructions for 16 rows of a warp are 118
+// cycles of an SM at full issue, about what the memory takes (111), but 16
+// warps, which is what the registers allow, keep 68 % of the issue slots busy.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -704,8 +709,8 @@ __device__ __forceinline__ void merge_slots(const Kv4AttendArgs& a, const Unit& 
 }
 
 // CTAs of an SM: two while a warp's sums fit 128 registers (4 heads).  With 8
-// heads of a unit, 4 x 131072 rows of 8 KV heads took 256 us with one CTA of 8
-// warps, 282 with 12 warps, 442 with two CTAs: the sums spill.
+// heads of a unit, 4 x 131072 rows of 8 KV heads in groups of 32 took 256 us
+// with one CTA of 8 warps, 282 with 12 warps, 442 with two CTAs: the sums spill.
 template <int NT>
 constexpr int kCtasPerSM = NT == 1 ? 2 : 1;
 
