@@ -102,7 +102,9 @@ cudaError_t dev_malloc(void** p, size_t bytes)
 {
     *p = nullptr;
     if (t_fault_left > 0 && --t_fault_left == 0) return cudaErrorMemoryAllocation;
-    return cudaMalloc(p, bytes);
+    const cudaError_t e = cudaMalloc(p, bytes);
+    if (e != cudaSuccess) cudaGetLastError();   // returned here, and not by the next launch as its own
+    return e;
 }
 
 #define CKV_CUDA(call)                                      \

@@ -31,7 +31,7 @@ __host__ __device__ inline int64_t kv4_rows(int n_max) { return ((int64_t)n_max 
 
 // A launch's own status.  cudaGetLastError() after <<<>>> would also report,
 // as this call's, what an earlier call of the thread left behind (an
-// allocation that failed, for instance).
+// that failed, for instance).
 template <class... Params, class... Args>
 cudaError_t launch_kernel(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const Args&... args)
 {

@@ -356,3 +356,18 @@ def test_rows_of_an_odd_number_of_heads(dtype, heads):
             np.testing.assert_array_equal(ref.codes(by[:, :, :T], bool(i)), code)
             np.testing.assert_array_equal(pa[:, :, :T, :, 0], scale)
             np.testing.assert_array_equal(pa[:, :, :T, :, 1], middle)
+
+
+def test_other_calls_after_a_failed_allocation():
+    # a failed ckv_create leaves nothing behind for calls that look at the last error after their launch
+    big = config(16, 64, 8, 1024, torch.bfloat16, sinks=4)
+    big.max_communities, big.kappa, big.budget, big.slack, big.pool_capacity = 16, 8, 64, 16, 2 ** 31 - 1
+    i64, i32, f32 = (dict(dtype=t, device="cuda") for t in (torch.int64, torch.int32, torch.float32))
+    rp, col, w = torch.tensor([0, 0, 1, 2], **i64), torch.tensor([0, 1], **i32), torch.ones(2, **f32)
+    labels = torch.zeros(3, **i32)
+    work = torch.empty(ckv.ckv_modularity_workspace(1), dtype=torch.uint8, device="cuda")
+    before = ckv.ckv_modularity(3, rp, col, w, labels, 1, 1.0, work)
+    with pytest.raises(ckv.CkvError) as e:
+        ckv.ckv_create(big)
+    assert e.value.status == ckv.CKV_ERR_OOM
+    assert ckv.ckv_modularity(3, rp, col, w, labels, 1, 1.0, work) == before
