@@ -911,8 +911,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM<NT>) k_kv4_attend(const _
             }
             // ---- arrival; the unit's last piece merges every slot.  A unit of
             // several pieces is the last one of its first CTA's share, so that
-            // CTA's counter is this unit's alone.  The barrier orders the CTA's stores before thread 0's fence, which
-            // makes them visible before its arrival; likewise the other way.
+            // CTA's counter is this unit's alone.  The barrier orders the CTA's
+            // stores before thread 0's fence, which makes them visible before
+            // its arrival; likewise the other way.
             __syncthreads();
             if (tid == 0) {
                 __threadfence();

@@ -30,8 +30,7 @@ constexpr int kRowCodes = kD / 2;              // code bytes of one row
 __host__ __device__ inline int64_t kv4_rows(int n_max) { return ((int64_t)n_max + 15) / 16 * 16; }
 
 // A launch's own status.  cudaGetLastError() after <<<>>> would also report,
-// as this call's, what an earlier call of the thread left behind (an
-// that failed, for instance).
+// as this call's, what an earlier call of the thread that failed left behind.
 template <class... Params, class... Args>
 cudaError_t launch_kernel(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const Args&... args)
 {
